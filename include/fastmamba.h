@@ -53,10 +53,11 @@ typedef enum fm_status {
     FM_ERR_SHAPE = 2,       /* unsupported or inconsistent sizes */
     FM_ERR_ALIGNMENT = 3,   /* pointer not 16-byte aligned */
     FM_ERR_WORKSPACE = 4,   /* workspace missing or too small */
-    FM_ERR_NONFINITE = 5,   /* a NaN or Inf reached an int8 activation quantiser */
+    FM_ERR_NONFINITE = 5,   /* a NaN or Inf reached an 8-bit quantiser */
     FM_ERR_TIMEOUT = 6,     /* a bounded device-side wait gave up */
     FM_ERR_CUDA = 7,        /* a CUDA runtime/driver call failed */
-    FM_ERR_UNSUPPORTED = 8  /* no sm_100 device, or driver entry point missing */
+    FM_ERR_UNSUPPORTED = 8, /* no sm_100 device, or driver entry point missing */
+    FM_ERR_INDEX = 9        /* a token id or a parent index was out of range */
 } fm_status;
 
 enum { FM_DYNAMIC = 0, FM_STATIC = 1 };
@@ -72,8 +73,10 @@ const char *fm_last_error(void);
  * precedence; the outputs and the carried states -- ssm_state, conv_state --
  * of the calls since the last read are then undefined), FM_ERR_NONFINITE (an activation row entering an int8
  * quantiser -- fm_hadamard_quant, fm_gate_norm_quant and the layers that
- * call them -- held a NaN or Inf; that row's codes and scale are then
- * undefined) or FM_ERR_CUDA (the synchronisation itself failed).  The word
+ * call them, fm_add_norm_quant and fm_prepare_linear_fp8 -- held a NaN or Inf;
+ * that row's codes and scale are then undefined), FM_ERR_INDEX (fm_embed_rows
+ * met a token id, or fm_reorder_rows a parent, out of range; what they do with
+ * it stands there) or FM_ERR_CUDA (the synchronisation itself failed).  The word
  * accumulates over every call on the device since it was last read. */
 fm_status fm_sync_status(fm_stream stream);
 /* Failure injection for tests of the bounded-wait path (the pages have no
@@ -595,6 +598,107 @@ fm_status fm_calibrate_layer(const fm_layer *L, const float *conv_b, int32_t *ex
                              int32_t *conv_bq, float *static_amax, const float *xcal, int B,
                              int T, int residual, float *out, void *ws, size_t ws_bytes,
                              fm_stream stream);
+
+/* ------------------------------------------------------------------ */
+/* the token loop around a stack                                       */
+/* ------------------------------------------------------------------ */
+/* Token ids in, next tokens out: embedding rows -> the stack -> residual
+ * addition + RMSNorm + 8-bit codes -> output head -> selection over beams ->
+ * the carried states follow their parents.  The pages stop at the stack; the
+ * pre-normed residual form is Mamba2's (the paper's references [2], [10]).
+ * None of these calls keeps anything between calls; all can be captured into
+ * a graph.  8-bit floating point is e4m3 (finite, largest value 448). */
+typedef enum fm_dtype { FM_F32 = 0, FM_BF16 = 1, FM_E4M3 = 2, FM_I8 = 3 } fm_dtype;
+
+/* r = fl(x + residual) in fp32 (r = x without a residual),
+ * y = norm_w r / sqrt(mean(r^2) + eps), and 8-bit codes q = nearest(y / s):
+ *   q_type FM_E4M3: s [M, ceil(K / 128)], s = fl(max|y| / 448) of each 128
+ *                   columns (the last block may be shorter): fm_fp8_gemm's A;
+ *   q_type FM_I8:   s [M], s = fl(max|y| / 127) of the row: fm_w8a8_gemm's A
+ *                   for weights prepared with rotate = 0.
+ * Codes and scales are those of exact arithmetic on r and norm_w, up to
+ * results within about 2^-50 of a tie (every sum and statistic is held in 64
+ * bits).  A block or row whose max|y| is below 2^-100 has s = 0 and codes 0.
+ *   x        [M, K] FM_F32 or FM_BF16, rows ldx elements apart
+ *   residual [M, K] fp32, rows ldr apart, or NULL
+ *   sum_out  [M, K] fp32, rows lds apart, or NULL: receives r; may be x or
+ *            residual itself (same address and row stride)
+ *   q        [M, K] dense
+ * K % 16 == 0, K <= 16384; row strides are multiples of 4 elements; eps in
+ * [1e-30, 1e30]. */
+fm_status fm_add_norm_quant(const void *x, fm_dtype x_type, int64_t ldx, const float *residual,
+                            int64_t ldr, int64_t M, int64_t K, const float *norm_w, double eps,
+                            fm_dtype q_type, void *q, float *s, float *sum_out, int64_t lds,
+                            fm_stream stream);
+
+/* Offline: W [N, K] fp32 -> Wq [N, K] e4m3 and s_w [ceil(N/128), ceil(K/128)],
+ * s = fl(max|W| / 448) of each 128 x 128 block, code = nearest(W / s); a block
+ * whose max|W| is below 2^-100 has s = 0 and codes 0.  K % 16 == 0. */
+fm_status fm_prepare_linear_fp8(const float *W, int64_t N, int64_t K, void *Wq, float *s_w,
+                                fm_stream stream);
+
+/* Matrix product in 8-bit floating point with a scale for each block of 128:
+ *   Y[m,n] = sum_b s_a[m,b] s_w[n/128,b] sum_{k in block b} A[m,k] W[n,k]
+ * with fp32 sums, each block's sum scaled in fp32 and the total rounded once
+ * to Y's type (FM_F32 or FM_BF16).
+ *   A [M, K] e4m3, s_a [M, ceil(K/128)]; W [N, K] e4m3, s_w [ceil(N/128),
+ *   ceil(K/128)]; Y rows ldy elements apart (any ldy >= N; other columns are
+ *   left as they were).  K % 16 == 0; M, N any (0: nothing is done). */
+fm_status fm_fp8_gemm(const void *A, const float *s_a, int64_t M, const void *W, const float *s_w,
+                      int64_t N, int64_t K, void *Y, fm_dtype y_type, int64_t ldy,
+                      fm_stream stream);
+
+/* Embedding rows: x[m] = scale table[ids[m]] in fp32, rows ldx apart.
+ *   table [V, K] FM_F32, FM_BF16, or FM_E4M3 with table_s [ceil(V/128),
+ *   ceil(K/128)] -- the layout of fm_prepare_linear_fp8, so an output head tied
+ *   to its embedding is stored once (each factor is multiplied and rounded in
+ *   turn: fl(fl(code s) scale)).
+ * An id of -1 (padding) gives a row of zeros; any other id outside [0, V) a
+ * row of zeros and FM_ERR_INDEX at the next fm_sync_status.
+ * K % 16 == 0; ldx % 4 == 0. */
+fm_status fm_embed_rows(const int32_t *ids, int64_t M, const void *table, fm_dtype type,
+                        const float *table_s, int64_t V, int64_t K, float scale, float *x,
+                        int64_t ldx, fm_stream stream);
+
+/* One step of beam search.  For logits [B, beams, V] (FM_F32 or FM_BF16, rows
+ * ld elements apart) and scores [B, beams], a candidate is worth
+ *   c[k,v] = scores[k] + l[k,v] - log sum_v' exp(l[k,v'])
+ * and each batch entry's n_out best are written in descending order, ties to
+ * the lowest k V + v: out_scores [B, n_out] = fl32(c) (at least the lowest
+ * fp32 value), parent (the beam k) and token (v) [B, n_out].  Candidates of one
+ * beam are ordered by their logits, those of different beams by c in 64 bits.
+ *   - A logit of -inf is no candidate, nor is any of a beam whose score is
+ *     -inf or NaN; a NaN logit counts as -inf, +inf as the largest fp32 value.
+ *   - finished [B, beams] or NULL: a beam with a nonzero flag has the one
+ *     candidate (eos, its score unchanged), whatever its logits.
+ *   - out_finished [B, n_out] or NULL: 1 where the parent was finished or the
+ *     token is eos.  eos: a token, or -1 (none; finished must be NULL then).
+ *   - With fewer than n_out candidates the slots j behind them hold score
+ *     -inf, parent j mod beams, token -1 and finished 0.
+ * out_scores may be scores and out_finished may be finished when
+ * n_out = beams.  beams and n_out in [1, 32]; n_out = beams = 1 is greedy
+ * decoding; beams = 1 with n_out > 1 opens a search.
+ * ws: device workspace of fm_beam_workspace_bytes(B, beams, V, n_out) bytes
+ * (0 for invalid sizes), written before it is read. */
+size_t fm_beam_workspace_bytes(int B, int beams, int64_t V, int n_out);
+fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t ld, int B, int beams, int64_t V,
+                         const float *scores, const uint8_t *finished, int eos, int n_out,
+                         float *out_scores, int32_t *parent, int32_t *token, uint8_t *out_finished,
+                         void *ws, size_t ws_bytes, fm_stream stream);
+
+/* The beams' carried states follow their parents: for every buffer i,
+ *   dst[i][b dst_beams + j] = src[i][b src_beams + parent[b dst_beams + j]]
+ * with rows of row_bytes[i] bytes (conv and SSM states of every layer, token
+ * histories, ...).  src[i] = dst[i] reorders in place (src_beams = dst_beams),
+ * without a second buffer; otherwise the two may not overlap, and src_beams 1
+ * spreads each sequence's state over its beams.  A parent outside
+ * [0, src_beams) leaves its row as it was and raises FM_ERR_INDEX at the next
+ * fm_sync_status.  src, dst and row_bytes are host arrays, read before the
+ * call returns; parent [B, dst_beams] is on the device.  Buffers of one call
+ * may not overlap each other.  Beams in [1, 32], B <= 65535. */
+fm_status fm_reorder_rows(const void *const *src, void *const *dst, const int64_t *row_bytes,
+                          int n_bufs, int B, int src_beams, int dst_beams, const int32_t *parent,
+                          fm_stream stream);
 
 #ifdef __cplusplus
 }

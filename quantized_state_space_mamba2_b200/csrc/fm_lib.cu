@@ -28,6 +28,9 @@
 #include "k_scan2.cuh"
 #include "k_ssd.cuh"
 #include "k_lq.cuh"
+#include "k_token.cuh"
+#include "k_beam.cuh"
+#include "k_fp8.cuh"
 
 using namespace fm;
 
@@ -118,6 +121,7 @@ extern "C" const char *fm_status_string(fm_status s) {
     case FM_ERR_TIMEOUT: return "FM_ERR_TIMEOUT";
     case FM_ERR_CUDA: return "FM_ERR_CUDA";
     case FM_ERR_UNSUPPORTED: return "FM_ERR_UNSUPPORTED";
+    case FM_ERR_INDEX: return "FM_ERR_INDEX";
   }
   return "FM_ERR_UNKNOWN";
 }
@@ -146,6 +150,8 @@ extern "C" fm_status fm_sync_status(fm_stream stream) {
     if (word & kErrTimeout) return fail(FM_ERR_TIMEOUT, "a bounded device wait gave up");
     if (word & kErrNonfinite)
       return fail(FM_ERR_NONFINITE, "a non-finite value (NaN or Inf) reached an int8 quantiser");
+    if (word & kErrIndex)
+      return fail(FM_ERR_INDEX, "a token id or a parent index was out of range");
   }
   return FM_OK;
 }
@@ -2233,3 +2239,5 @@ extern "C" fm_status fm_calibrate_layer(const fm_layer *L, const float *conv_b, 
                                     nullptr),
                      s);
 }
+
+#include "fm_token_api.cuh"

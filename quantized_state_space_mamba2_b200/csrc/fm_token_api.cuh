@@ -1,0 +1,247 @@
+// fm_token_api.cuh -- host side of the token-loop entry points (included at the
+// end of fm_lib.cu: argument checks, workspace carving and launches).
+
+static bool dtype_in(fm_dtype t, fm_dtype a, fm_dtype b, fm_dtype c) {
+  return t == a || t == b || t == c;
+}
+
+// ------------------------------------------------------------------ add + norm + codes
+template <typename TX>
+static fm_status launch_add_norm(const void *x, int64_t ldx, const float *residual, int64_t ldr,
+                                 int64_t M, int K, const float *w, double eps, bool e4m3, void *q,
+                                 float *s, float *sum, int64_t lds, cudaStream_t st) {
+  auto kern = e4m3 ? k_add_norm_quant<TX, true> : k_add_norm_quant<TX, false>;
+  FM_TRY(launch_ex("k_add_norm_quant", kern, (unsigned)M, 32 * ((K + kNormCols - 1) / kNormCols), 0,
+                   st, (const TX *)x, (long long)ldx, residual, (long long)ldr, K, w, eps,
+                   (uint8_t *)q, s, sum, (long long)lds));
+  return launched("k_add_norm_quant");
+}
+
+extern "C" fm_status fm_add_norm_quant(const void *x, fm_dtype x_type, int64_t ldx,
+                                       const float *residual, int64_t ldr, int64_t M, int64_t K,
+                                       const float *norm_w, double eps, fm_dtype q_type, void *q,
+                                       float *s, float *sum_out, int64_t lds, fm_stream stream) {
+  if (x_type != FM_F32 && x_type != FM_BF16)
+    return fail(FM_ERR_INVALID_ARG, "%s: x must be fp32 or bf16", __func__);
+  if (q_type != FM_I8 && q_type != FM_E4M3)
+    return fail(FM_ERR_INVALID_ARG, "%s: q must be int8 or e4m3", __func__);
+  if (!(eps >= 1e-30 && eps <= 1e30))  // the kernel's 2^e = 2^exponent(rstd) stays an fp32 number
+    return fail(FM_ERR_INVALID_ARG, "%s: eps must lie in [1e-30, 1e30]", __func__);
+  if (M < 0 || M > 0x7FFFFFFF || K <= 0 || K % 16 || K > kNormMaxK)
+    return fail(FM_ERR_SHAPE, "%s: need 0 <= M < 2^31 and K a multiple of 16, <= %d", __func__,
+                kNormMaxK);
+  if (ldx < K || ldx % 4 || (residual && (ldr < K || ldr % 4)) || (sum_out && (lds < K || lds % 4)))
+    return fail(FM_ERR_SHAPE, "%s: row strides must be multiples of 4, at least K", __func__);
+  if (M == 0) return FM_OK;
+  NEED(x);
+  OPT(residual);
+  NEED(norm_w);
+  NEED(q);
+  NEED(s);
+  OPT(sum_out);
+  auto go = x_type == FM_F32 ? launch_add_norm<float> : launch_add_norm<__nv_bfloat16>;
+  return go(x, ldx, residual, ldr, M, (int)K, norm_w, eps, q_type == FM_E4M3, q, s, sum_out, lds,
+            (cudaStream_t)stream);
+}
+
+// ------------------------------------------------------------------ block-scaled e4m3 product
+extern "C" fm_status fm_prepare_linear_fp8(const float *W, int64_t N, int64_t K, void *Wq,
+                                           float *s_w, fm_stream stream) {
+  if (N <= 0 || K <= 0 || K % 16 || K > 0x7FFFFFFF || (N + 127) / 128 > 65535)
+    return fail(FM_ERR_SHAPE, "%s: need N in [1, 65535 * 128] and K a positive multiple of 16",
+                __func__);
+  NEED(W);
+  NEED(Wq);
+  NEED(s_w);
+  const dim3 grid((unsigned)((K + 127) / 128), (unsigned)((N + 127) / 128));
+  FM_TRY(launch_ex("k_prepare_linear_fp8", k_prepare_linear_fp8, grid, 256, 0, (cudaStream_t)stream,
+                   W, (long long)N, (int)K, (uint8_t *)Wq, s_w));
+  return launched("k_prepare_linear_fp8");
+}
+
+extern "C" fm_status fm_fp8_gemm(const void *A, const float *s_a, int64_t M, const void *W,
+                                 const float *s_w, int64_t N, int64_t K, void *Y, fm_dtype y_type,
+                                 int64_t ldy, fm_stream stream) {
+  if (y_type != FM_F32 && y_type != FM_BF16)
+    return fail(FM_ERR_INVALID_ARG, "%s: Y must be fp32 or bf16", __func__);
+  if (M < 0 || N < 0 || M > 65535 * 64 || N > 0x7FFFFFFF || K <= 0 || K % 16 || K > 0x7FFFFFFF)
+    return fail(FM_ERR_SHAPE,
+                "%s: need 0 <= M <= 65535 * 64, 0 <= N < 2^31 and K a positive multiple of 16",
+                __func__);
+  if (ldy < N) return fail(FM_ERR_SHAPE, "%s: ldy is less than N", __func__);
+  if (M == 0 || N == 0) return FM_OK;
+  NEED(A);
+  NEED(s_a);
+  NEED(W);
+  NEED(s_w);
+  NEED(Y);
+  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
+  if (y_type == FM_F32)
+    FM_TRY(launch_ex("k_fp8_gemm", k_fp8_gemm_simple<float>, grid, 256, 0, (cudaStream_t)stream,
+                     (const uint8_t *)A, s_a, (long long)M, (const uint8_t *)W, s_w, (long long)N,
+                     (int)K, (float *)Y, (long long)ldy));
+  else
+    FM_TRY(launch_ex("k_fp8_gemm", k_fp8_gemm_simple<__nv_bfloat16>, grid, 256, 0,
+                     (cudaStream_t)stream, (const uint8_t *)A, s_a, (long long)M,
+                     (const uint8_t *)W, s_w, (long long)N, (int)K, (__nv_bfloat16 *)Y,
+                     (long long)ldy));
+  return launched("k_fp8_gemm");
+}
+
+// ------------------------------------------------------------------ beam selection
+static size_t beam_ws_keys(int64_t rows, int n_out) {
+  return ((size_t)rows * n_out * 8 + 255) / 256 * 256;
+}
+static bool beam_sizes_ok(int B, int beams, int64_t V, int n_out) {
+  return B >= 0 && beams >= 1 && beams <= kBeamMax && n_out >= 1 && n_out <= kBeamMax && V >= 1 &&
+         V <= 0x7FFFFFFF && (int64_t)B * beams <= 0x7FFFFFFF;
+}
+
+extern "C" size_t fm_beam_workspace_bytes(int B, int beams, int64_t V, int n_out) {
+  if (!beam_sizes_ok(B, beams, V, n_out)) return 0;
+  const int64_t rows = (int64_t)B * beams;
+  return beam_ws_keys(rows, n_out) + (size_t)rows * 8;
+}
+
+extern "C" fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t ld, int B, int beams,
+                                    int64_t V, const float *scores, const uint8_t *finished,
+                                    int eos, int n_out, float *out_scores, int32_t *parent,
+                                    int32_t *token, uint8_t *out_finished, void *ws,
+                                    size_t ws_bytes, fm_stream stream) {
+  if (type != FM_F32 && type != FM_BF16)
+    return fail(FM_ERR_INVALID_ARG, "%s: logits must be fp32 or bf16", __func__);
+  if (!beam_sizes_ok(B, beams, V, n_out))
+    return fail(FM_ERR_SHAPE, "%s: need beams and n_out in [1, %d], V in [1, 2^31) and B * beams < 2^31",
+                __func__, kBeamMax);
+  if (ld < V) return fail(FM_ERR_SHAPE, "%s: ld is less than V", __func__);
+  if (eos < -1 || eos >= V || (finished && eos < 0))
+    return fail(FM_ERR_INVALID_ARG, "%s: eos must be a token (or -1 where no beam is finished)",
+                __func__);
+  if (B == 0) return FM_OK;
+  NEED(logits);
+  NEED(scores);
+  OPT(finished);
+  NEED(out_scores);
+  NEED(parent);
+  NEED(token);
+  OPT(out_finished);
+  if ((out_scores == scores || (finished && out_finished == finished)) && n_out != beams)
+    return fail(FM_ERR_INVALID_ARG, "%s: outputs may replace the inputs only where n_out = beams",
+                __func__);
+  const size_t need = fm_beam_workspace_bytes(B, beams, V, n_out);
+  if (!ws || ws_bytes < need)
+    return fail(FM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", __func__, need);
+  NEED(ws);
+  const int64_t rows = (int64_t)B * beams;
+  unsigned long long *keys = (unsigned long long *)ws;
+  double *lse = (double *)((char *)ws + beam_ws_keys(rows, n_out));
+  cudaStream_t st = (cudaStream_t)stream;
+  if (type == FM_F32)
+    FM_TRY(launch_ex("k_beam_rows", k_beam_rows<float>, (unsigned)rows, kBeamThreads, 0, st,
+                     (const float *)logits, (long long)ld, (unsigned)V, n_out, keys, lse));
+  else
+    FM_TRY(launch_ex("k_beam_rows", k_beam_rows<__nv_bfloat16>, (unsigned)rows, kBeamThreads, 0, st,
+                     (const __nv_bfloat16 *)logits, (long long)ld, (unsigned)V, n_out, keys, lse));
+  FM_TRY(launched("k_beam_rows"));
+  FM_TRY(launch_ex("k_beam_merge", k_beam_merge, (unsigned)B, 32, 0, st,
+                   (const unsigned long long *)keys, (const double *)lse, beams, scores, finished,
+                   eos, n_out, out_scores, parent, token, out_finished));
+  return launched("k_beam_merge");
+}
+
+// ------------------------------------------------------------------ state reordering
+template <typename U>
+static fm_status launch_reorder(const ReorderArgs &a, unsigned blocks, int B, cudaStream_t st) {
+  auto kern = a.dst_beams <= 4    ? k_reorder_rows<U, 4>
+              : a.dst_beams <= 8  ? k_reorder_rows<U, 8>
+              : a.dst_beams <= 16 ? k_reorder_rows<U, 16>
+                                  : k_reorder_rows<U, 32>;
+  FM_TRY(launch_ex("k_reorder_rows", kern, dim3(blocks, (unsigned)B), kReorderThreads, 0, st, a));
+  return launched("k_reorder_rows");
+}
+
+extern "C" fm_status fm_reorder_rows(const void *const *src, void *const *dst,
+                                     const int64_t *row_bytes, int n_bufs, int B, int src_beams,
+                                     int dst_beams, const int32_t *parent, fm_stream stream) {
+  if (n_bufs < 0 || (n_bufs > 0 && (!src || !dst || !row_bytes)))
+    return fail(FM_ERR_INVALID_ARG, "%s: src, dst or row_bytes is null", __func__);
+  if (B < 0 || B > 65535 || src_beams < 1 || src_beams > kReorderBeams || dst_beams < 1 ||
+      dst_beams > kReorderBeams)
+    return fail(FM_ERR_SHAPE, "%s: need B <= 65535 and beams in [1, %d]", __func__, kReorderBeams);
+  if (B == 0 || n_bufs == 0) return FM_OK;
+  NEED(parent);
+  for (int i = 0; i < n_bufs; ++i) {
+    if (row_bytes[i] < 0 || row_bytes[i] > (int64_t)1 << 36)
+      return fail(FM_ERR_SHAPE, "%s: row_bytes[%d] is negative or above 2^36", __func__, i);
+    if (row_bytes[i] && (!src[i] || !dst[i]))
+      return fail(FM_ERR_INVALID_ARG, "%s: buffer %d is null", __func__, i);
+    if (!aligned16(src[i]) || !aligned16(dst[i]))
+      return fail(FM_ERR_ALIGNMENT, "%s: buffer %d is not 16-byte aligned", __func__, i);
+    const uintptr_t s0 = (uintptr_t)src[i], d0 = (uintptr_t)dst[i];
+    if (s0 == d0) {
+      if (src_beams != dst_beams)
+        return fail(FM_ERR_INVALID_ARG, "%s: buffer %d in place needs src_beams = dst_beams",
+                    __func__, i);
+    } else if (s0 < d0 + (uintptr_t)(row_bytes[i] * B * dst_beams) &&
+               d0 < s0 + (uintptr_t)(row_bytes[i] * B * src_beams)) {
+      return fail(FM_ERR_INVALID_ARG, "%s: src and dst of buffer %d overlap", __func__, i);
+    }
+  }
+  // one launch per 128 buffers of the same unit: 16 bytes where the rows are
+  // multiples of 16 (every state of the library), else 4 or 1
+  for (int unit : {16, 4, 1}) {
+    ReorderArgs a = {};
+    a.src_beams = src_beams;
+    a.dst_beams = dst_beams;
+    a.parent = parent;
+    int64_t blocks = 0;
+    auto flush = [&]() -> fm_status {
+      if (a.n == 0) return FM_OK;
+      a.first[a.n] = (unsigned)blocks;
+      fm_status st = unit == 16  ? launch_reorder<uint4>(a, (unsigned)blocks, B, (cudaStream_t)stream)
+                     : unit == 4 ? launch_reorder<uint32_t>(a, (unsigned)blocks, B, (cudaStream_t)stream)
+                                 : launch_reorder<uint8_t>(a, (unsigned)blocks, B, (cudaStream_t)stream);
+      a.n = 0;
+      blocks = 0;
+      return st;
+    };
+    for (int i = 0; i < n_bufs; ++i) {
+      const int64_t rb = row_bytes[i];
+      if (rb == 0 || unit != (rb % 16 == 0 ? 16 : rb % 4 == 0 ? 4 : 1)) continue;
+      const int64_t units = rb / unit, nb = (units + kReorderThreads - 1) / kReorderThreads;
+      if (units > 0xFFFFFFFFll || nb > 0x7FFFFFFFll)
+        return fail(FM_ERR_SHAPE, "%s: rows of buffer %d are too long", __func__, i);
+      if (a.n == kReorderBufs || blocks + nb > 0x7FFFFFFFll) FM_TRY(flush());
+      a.src[a.n] = src[i];
+      a.dst[a.n] = dst[i];
+      a.first[a.n] = (unsigned)blocks;
+      a.units[a.n] = (unsigned)units;
+      ++a.n;
+      blocks += nb;
+    }
+    FM_TRY(flush());
+  }
+  return FM_OK;
+}
+
+// ------------------------------------------------------------------ embedding rows
+extern "C" fm_status fm_embed_rows(const int32_t *ids, int64_t M, const void *table, fm_dtype type,
+                                   const float *table_s, int64_t V, int64_t K, float scale,
+                                   float *x, int64_t ldx, fm_stream stream) {
+  if (!dtype_in(type, FM_F32, FM_BF16, FM_E4M3))
+    return fail(FM_ERR_INVALID_ARG, "%s: the table must be fp32, bf16 or e4m3", __func__);
+  if (M < 0 || (M + 3) / 4 > 0x7FFFFFFF || V < 1 || V > 0x7FFFFFFF || K <= 0 || K % 16 ||
+      K > 0x7FFFFFFF)
+    return fail(FM_ERR_SHAPE, "%s: need V in [1, 2^31) and K a positive multiple of 16", __func__);
+  if (ldx < K || ldx % 4)
+    return fail(FM_ERR_SHAPE, "%s: ldx must be a multiple of 4, at least K", __func__);
+  if (M == 0) return FM_OK;
+  NEED(ids);
+  NEED(table);
+  if (type == FM_E4M3) NEED(table_s);
+  NEED(x);
+  auto kern = type == FM_F32 ? k_embed_rows<0> : type == FM_BF16 ? k_embed_rows<1> : k_embed_rows<2>;
+  FM_TRY(launch_ex("k_embed_rows", kern, (unsigned)((M + 3) / 4), 128, 0, (cudaStream_t)stream, ids,
+                   (long long)M, table, table_s, (long long)V, (int)K, scale, x, (long long)ldx));
+  return launched("k_embed_rows");
+}

@@ -1,0 +1,332 @@
+// k_token.cuh -- row-wise kernels of the token loop around a stack: residual
+// addition + RMSNorm + 8-bit codes, embedding rows, and the reordering of
+// carried states after a beam selection.  All three are bound by memory.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include "fm_common.cuh"
+
+namespace fm {
+
+// ------------------------------------------------------------ fp8 helpers
+// two fp32 -> two e4m3 codes (round to nearest even, saturating): lo in bits 0-7
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// four e4m3 codes -> fp32 (exact)
+__device__ __forceinline__ float4 e4m3x4_f32(uint32_t c) {
+  uint32_t a, b;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(c));
+  const float2 lo = __half22float2(*reinterpret_cast<__half2 *>(&a));
+  const float2 hi = __half22float2(*reinterpret_cast<__half2 *>(&b));
+  return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+
+// four consecutive elements as fp32
+__device__ __forceinline__ float4 load4(const float *p) {
+  return *reinterpret_cast<const float4 *>(p);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+}
+
+// ------------------------------------------------------------ add + norm + codes
+// r = fl(x + residual); y = r w / sqrt(mean(r^2) + eps); codes q = nearest(y / s)
+// with s = fl(max|y| / 448) per 128 columns (e4m3) or fl(max|y| / 127) per row
+// (int8).  The codes are those of the exact quotient (64-bit sums and
+// statistics; an fp32 product decides a code unless it lies so near the middle
+// between two codes that its rounding could, and that element is then redone
+// in 64 bits), so they do not depend on the order of any fp32 sum.
+//
+// One CTA per row, one warp per 512 columns: 8 lanes hold a 128-column block,
+// lane l of them the four groups of 4 columns at 4 l + 32 j, so every load of
+// the 8 lanes is one run of 128 bytes (fp32) and a block's maximum takes three
+// shuffles.  The row stays in registers: one read of x, residual and w, one
+// write of the sum, the codes and the scales.
+constexpr int kNormCols = 512;   // columns per warp
+constexpr int kNormMaxK = 32 * kNormCols;
+constexpr float kNormTiny = 7.888609052210118e-31f;  // 2^-100: a smaller max|y| counts as zero
+
+__device__ __forceinline__ float group8_max(float v) {
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// v = r w c in 64 bits, rounded to fp32 towards zero with the lost bits kept as
+// a last 1: a later rounding to fewer than 22 bits is then that of v itself
+__device__ __forceinline__ float sticky_product(float r, float w, double c) {
+  const double v = __dmul_rn(__dmul_rn((double)r, (double)w), c);
+  float f = __double2float_rz(v);
+  if ((double)f != v) f = __uint_as_float(__float_as_uint(f) | 1u);
+  return f;
+}
+
+// e4m3: t = p cf is within 3 ulp of y / s.  A tie of two codes has the low 20
+// of its 23 fraction bits at 0x80000; below the normal codes (|t| < 2^-6) and
+// not under half the smallest one (2^-10) the spacing is fixed, and the few
+// values there are always redone.
+__device__ __forceinline__ float e4m3_arg(float p, float cf, float r, float w, double c) {
+  float t = __fmul_rn(p, cf);
+  const uint32_t a = __float_as_uint(t) & 0x7FFFFFFFu;
+  if ((a & 0xFFFFFu) - 0x7FFF8u <= 16u || a - 0x3A7FF000u < 0x3C800000u - 0x3A7FF000u)
+    t = sticky_product(r, w, c);
+  return t;
+}
+// int8: t = p cf is within 127 * 3 * 2^-24 < 2^-15 of y / s
+__device__ __forceinline__ int int8_code(float p, float cf, float r, float w, double c) {
+  float t = __fmul_rn(p, cf);
+  if (fabsf(__fsub_rn(t, rintf(t))) > 0.5f - 0x1p-14f) t = sticky_product(r, w, c);
+  return quant127(t);
+}
+
+template <typename TX, bool E4M3>
+__global__ void __launch_bounds__(1024) k_add_norm_quant(
+    const TX *x, long long ldx, const float *residual, long long ldr, int K,
+    const float *__restrict__ norm_w, double eps, uint8_t *__restrict__ q, float *__restrict__ s,
+    float *sum_out, long long lds) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ double s_ss[32];
+  __shared__ float s_max[32], s_rem[32];
+  const long long row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  const int col0 = warp * kNormCols + (lane >> 3) * 128 + (lane & 7) * 4;
+  float r[16], w[16];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = col0 + 32 * j;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v, g = v;
+    if (c < K) {
+      v = load4(x + row * ldx + c);
+      if (residual) u = load4(residual + row * ldr + c);
+      g = load4(norm_w + c);
+    }
+    if (residual) {
+      v.x = __fadd_rn(v.x, u.x); v.y = __fadd_rn(v.y, u.y);
+      v.z = __fadd_rn(v.z, u.z); v.w = __fadd_rn(v.w, u.w);
+    }
+    r[4 * j] = v.x; r[4 * j + 1] = v.y; r[4 * j + 2] = v.z; r[4 * j + 3] = v.w;
+    w[4 * j] = g.x; w[4 * j + 1] = g.y; w[4 * j + 2] = g.z; w[4 * j + 3] = g.w;
+    if (sum_out && c < K) *reinterpret_cast<float4 *>(sum_out + row * lds + c) = v;
+  }
+  double ss = 0.0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ss = __fma_rn((double)r[i], (double)r[i], ss);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+  if (lane == 0) s_ss[warp] = ss;
+  __syncthreads();
+  ss = lane < nw ? s_ss[lane] : 0.0;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+  if (!(ss <= 1.7e308) && threadIdx.x == 0) raise_error(kErrNonfinite);
+  const double rstd = __drcp_rn(__dsqrt_rn(__dadd_rn(__ddiv_rn(ss, (double)K), eps)));
+  // rstd = rs 2^e with rs in [1, 2): r 2^e is exact and at most about sqrt(K),
+  // so the products below cannot overflow whatever the row's magnitude
+  const long long rb = __double_as_longlong(rstd);
+  const int e = (int)((rb >> 52) & 0x7FF) - 1023;
+  const double rs = __longlong_as_double((rb & 0xFFFFFFFFFFFFFll) | 0x3FF0000000000000ll);
+  const float pe = ldexpf(1.0f, e);
+  float p[16], m = 0.0f;
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    r[i] = __fmul_rn(r[i], pe);
+    p[i] = __fmul_rn(r[i], w[i]);
+    finite = finite && fabsf(p[i]) <= 3.402823466e38f;
+    m = fmaxf(m, fabsf(p[i]));
+  }
+  if (!finite) raise_error(kErrNonfinite);
+  // max|r w| exactly: the largest fp32 product plus the largest exact
+  // remainder among the elements that round to it
+  m = group8_max(m);
+  if (!E4M3) {
+    m = warp_max(m);
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    m = warp_max(lane < nw ? s_max[lane] : 0.0f);
+  }
+  float rem = -3.0e38f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (fabsf(p[i]) == m) rem = fmaxf(rem, __fmaf_rn(fabsf(r[i]), fabsf(w[i]), -m));
+  rem = group8_max(rem);
+  if (!E4M3) {
+    rem = warp_max(rem);
+    if (lane == 0) s_rem[warp] = rem;
+    __syncthreads();
+    rem = warp_max(lane < nw ? s_rem[lane] : -3.0e38f);
+  }
+  double amax = __dmul_rn(__dadd_rn((double)m, (double)rem), rs);
+  // below 2^-100 (which covers every p that lost bits to underflow): zeros
+  if (!(m > 0.0f) || amax < (double)kNormTiny) amax = 0.0;
+  const float sc = (float)__ddiv_rn(amax, E4M3 ? 448.0 : 127.0);
+  const double c = sc > 0.0f ? __ddiv_rn(rs, (double)sc) : 0.0;
+  const float cf = (float)c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int col = col0 + 32 * j;
+    uint32_t o;
+    if constexpr (E4M3) {
+      float t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        t[i] = e4m3_arg(p[4 * j + i], cf, r[4 * j + i], w[4 * j + i], c);
+      o = e4m3x2(t[0], t[1]) | (e4m3x2(t[2], t[3]) << 16);
+    } else {
+      o = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o |= (uint32_t)(int8_code(p[4 * j + i], cf, r[4 * j + i], w[4 * j + i], c) & 0xFF) << (8 * i);
+    }
+    if (col < K) *reinterpret_cast<uint32_t *>(q + row * K + col) = o;
+  }
+  if constexpr (E4M3) {
+    const int nb = (K + 127) / 128, b = warp * 4 + (lane >> 3);
+    if ((lane & 7) == 0 && b < nb) s[row * nb + b] = sc;
+  } else {
+    if (threadIdx.x == 0) s[row] = sc;
+  }
+}
+
+// Offline: W [N, K] fp32 -> e4m3 codes and one scale per 128 x 128 block,
+// s = fl(max|W| / 448), code = nearest(W / s).  One CTA of 256 threads per block.
+__global__ void __launch_bounds__(256) k_prepare_linear_fp8(const float *__restrict__ W, long long N,
+                                                            int K, uint8_t *__restrict__ Wq,
+                                                            float *__restrict__ s_w) {
+  __shared__ float s_red[8];
+  const int k0 = blockIdx.x * 128;
+  const long long n0 = (long long)blockIdx.y * 128;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int k = k0 + 4 * lane;
+  float a = 0.0f;
+  bool finite = true;
+  for (int i = warp; i < 128; i += 8)
+    if (n0 + i < N && k < K) {
+      const float4 v = load4(W + (n0 + i) * K + k);
+      const float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+      finite = finite && fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) <= 3.402823466e38f;
+      a = fmaxf(a, m);
+    }
+  if (!finite) raise_error(kErrNonfinite);
+  a = warp_max(a);
+  if (lane == 0) s_red[warp] = a;
+  __syncthreads();
+  a = warp_max(lane < 8 ? s_red[lane] : 0.0f);
+  if (a < kNormTiny) a = 0.0f;
+  const float s = (float)__ddiv_rn((double)a, 448.0);
+  const double c = s > 0.0f ? __drcp_rn((double)s) : 0.0;
+  for (int i = warp; i < 128; i += 8)
+    if (n0 + i < N && k < K) {
+      const float4 v = load4(W + (n0 + i) * K + k);
+      const float t0 = sticky_product(v.x, 1.0f, c), t1 = sticky_product(v.y, 1.0f, c);
+      const float t2 = sticky_product(v.z, 1.0f, c), t3 = sticky_product(v.w, 1.0f, c);
+      *reinterpret_cast<uint32_t *>(Wq + (n0 + i) * K + k) = e4m3x2(t0, t1) | (e4m3x2(t2, t3) << 16);
+    }
+  if (threadIdx.x == 0) s_w[(long long)blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// ------------------------------------------------------------ embedding rows
+// x[m] = scale * table[ids[m]]; an id of -1 (padding) gives zeros, any other id
+// outside [0, V) zeros and the device error word.  One warp per row.
+// TYPE 0: fp32 table, 1: bf16, 2: e4m3 codes with a scale per 128 x 128 block.
+template <int TYPE>
+__global__ void __launch_bounds__(128) k_embed_rows(const int32_t *__restrict__ ids, long long M,
+                                                    const void *__restrict__ table,
+                                                    const float *__restrict__ table_s, long long V,
+                                                    int K, float scale, float *__restrict__ x,
+                                                    long long ldx) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= M) return;
+  const long long id = ids[row];
+  const bool live = id >= 0 && id < V;
+  if (!live && id != -1 && lane == 0) raise_error(kErrIndex);
+  const int nb = (K + 127) / 128;
+  for (int c = 4 * lane; c < K; c += 128) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      if constexpr (TYPE == 0) v = load4((const float *)table + id * K + c);
+      if constexpr (TYPE == 1) v = load4((const __nv_bfloat16 *)table + id * K + c);
+      if constexpr (TYPE == 2) {
+        v = e4m3x4_f32(*reinterpret_cast<const uint32_t *>((const uint8_t *)table + id * K + c));
+        const float s = table_s[(id >> 7) * nb + (c >> 7)];
+        v.x = __fmul_rn(v.x, s); v.y = __fmul_rn(v.y, s);
+        v.z = __fmul_rn(v.z, s); v.w = __fmul_rn(v.w, s);
+      }
+      v.x = __fmul_rn(v.x, scale); v.y = __fmul_rn(v.y, scale);
+      v.z = __fmul_rn(v.z, scale); v.w = __fmul_rn(v.w, scale);
+    }
+    *reinterpret_cast<float4 *>(x + row * ldx + c) = v;
+  }
+}
+
+// ------------------------------------------------------------ state reordering
+// dst[b, j] = src[b, parent[b, j]] for every buffer, in place where src = dst.
+// A thread owns one unit (16 bytes where rows allow it) of a row's columns for
+// all the beams of one batch entry: it reads every beam's new value before it
+// writes any, so no second buffer and no order between threads is needed.
+// In place, a beam that keeps its own state is neither read nor written.  A
+// parent outside the source's beams leaves the row as it was and sets the
+// device error word.
+constexpr int kReorderBufs = 128;  // buffers per launch
+constexpr int kReorderBeams = 32;
+constexpr int kReorderThreads = 256;
+
+struct ReorderArgs {
+  const void *src[kReorderBufs];
+  void *dst[kReorderBufs];
+  unsigned first[kReorderBufs + 1];  // first block of each buffer
+  unsigned units[kReorderBufs];      // units per row
+  int n, src_beams, dst_beams;
+  const int32_t *parent;
+};
+
+template <typename U, int G>
+__global__ void __launch_bounds__(kReorderThreads)
+    k_reorder_rows(const __grid_constant__ ReorderArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  int lo = 0, hi = a.n;  // the buffer of this block
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.first[mid] <= blockIdx.x) lo = mid;
+    else hi = mid;
+  }
+  const unsigned units = a.units[lo];
+  const unsigned col = (blockIdx.x - a.first[lo]) * kReorderThreads + threadIdx.x;
+  if (col >= units) return;
+  const U *src = (const U *)a.src[lo] + (size_t)blockIdx.y * a.src_beams * units + col;
+  U *dst = (U *)a.dst[lo] + (size_t)blockIdx.y * a.dst_beams * units + col;
+  const bool same = a.src[lo] == a.dst[lo];
+  const int32_t *par = a.parent + (size_t)blockIdx.y * a.dst_beams;
+  U v[G];
+  unsigned moved = 0;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    if (j < a.dst_beams) {
+      const int p = par[j];
+      if (p < 0 || p >= a.src_beams) {
+        if (col == 0) raise_error(kErrIndex);
+      } else if (!same || p != j) {
+        v[j] = src[(size_t)p * units];
+        moved |= 1u << j;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < G; ++j)
+    if (moved >> j & 1u) dst[(size_t)j * units] = v[j];
+}
+
+}  // namespace fm

@@ -18,7 +18,7 @@ SO_PATH = os.path.join(_HERE, "libfastmamba.so")
 FM_DYNAMIC, FM_STATIC = 0, 1
 STATUS = {0: "FM_OK", 1: "FM_ERR_INVALID_ARG", 2: "FM_ERR_SHAPE", 3: "FM_ERR_ALIGNMENT",
           4: "FM_ERR_WORKSPACE", 5: "FM_ERR_NONFINITE", 6: "FM_ERR_TIMEOUT", 7: "FM_ERR_CUDA",
-          8: "FM_ERR_UNSUPPORTED"}
+          8: "FM_ERR_UNSUPPORTED", 9: "FM_ERR_INDEX"}
 
 # every entry point the header declares
 EXPORTS = (
@@ -34,6 +34,8 @@ EXPORTS = (
     "fm_set_gemm_tile", "fm_set_xbc_exponents", "fm_conv1d_pot_tok", "fm_ssm_scan_pot_tok",
     "fm_scan_workspace_bytes_tok", "fm_set_pdl", "fm_set_lq_scan_cpw", "fm_set_gemm_cluster",
     "fm_stack_prefill", "fm_stack_workspace_bytes", "fm_stack_prefill_host",
+    "fm_add_norm_quant", "fm_prepare_linear_fp8", "fm_fp8_gemm", "fm_embed_rows",
+    "fm_beam_workspace_bytes", "fm_beam_select", "fm_reorder_rows",
 )
 NOALLOC_SCRATCH_BYTES = 16 << 20  # FM_NOALLOC_SCRATCH_BYTES
 
@@ -131,6 +133,14 @@ def load():
         "fm_scan_workspace_bytes_tok": (SZ, [sp, I, I]),
         "fm_lq_mixer_prefill": (I, [lp, C.POINTER(fm_lq_params), _P, I, I, I, _P, _P, _P, _P,
                                     SZ, _P]),
+        "fm_add_norm_quant": (I, [_P, I, I64, _P, I64, I64, I64, _P, C.c_double, I, _P, _P, _P, I64,
+                                  _P]),
+        "fm_prepare_linear_fp8": (I, [_P, I64, I64, _P, _P, _P]),
+        "fm_fp8_gemm": (I, [_P, _P, I64, _P, _P, I64, I64, _P, I, I64, _P]),
+        "fm_embed_rows": (I, [_P, I64, _P, I, _P, I64, I64, C.c_float, _P, I64, _P]),
+        "fm_beam_workspace_bytes": (SZ, [I, I, I64, I]),
+        "fm_beam_select": (I, [_P, I, I64, I, I, I64, _P, _P, I, I, _P, _P, _P, _P, _P, SZ, _P]),
+        "fm_reorder_rows": (I, [_P, _P, _P, I, I, I, I, _P, _P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -485,3 +495,153 @@ def lq_mixer_prefill(layer: fm_layer, params: fm_lq_params, x, B, T, residual, c
     _check(load().fm_lq_mixer_prefill(C.byref(layer), C.byref(params), _p(x), B, T, residual,
                                       _p(conv_state), _p(ssm_state), _p(out), _p(ws),
                                       ws.numel() * ws.element_size(), _s(stream)))
+
+
+# ------------------------------------------------------------------ the token loop
+FM_F32, FM_BF16, FM_E4M3, FM_I8 = 0, 1, 2, 3
+_DTYPES = {torch.float32: FM_F32, torch.bfloat16: FM_BF16, torch.float8_e4m3fn: FM_E4M3,
+           torch.int8: FM_I8}
+BEAM_MAX = 32  # beams and n_out of beam_select and reorder_rows
+
+
+def blocks128(n: int) -> int:
+    """Number of 128-wide scale blocks of n columns (or rows)."""
+    return (n + 127) // 128
+
+
+def _want(name, t, shape, *dtypes):
+    """A tensor argument's shape, type and device: a CUDA tensor on the current
+    device (the call launches there), rows of any stride, unit column stride."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: libfastmamba takes CUDA tensors on the current device")
+    return C.c_void_p(t.data_ptr())
+
+
+def _dense(name, t, shape, *dtypes):
+    p = _want(name, t, shape, *dtypes)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is required")
+    return p
+
+
+def _rows(name, t, shape, *dtypes):
+    """(pointer, row stride in elements) of a matrix with unit column stride."""
+    p = _want(name, t, shape, *dtypes)
+    if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: unit column stride is required")
+    return p, t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+
+
+def add_norm_quant(x, norm_w, q, s, residual=None, sum_out=None, eps=1e-5, stream=None):
+    """r = x + residual; RMSNorm(r) * norm_w as 8-bit codes.  q int8 [M, K] with
+    s [M] (a scale per row), or float8_e4m3fn with s [M, blocks128(K)] (one per
+    128 columns); sum_out (may be x or residual) receives r."""
+    M, K = x.shape
+    px, ldx = _rows("x", x, (M, K), torch.float32, torch.bfloat16)
+    pr, ldr = (None, 0) if residual is None else _rows("residual", residual, (M, K), torch.float32)
+    po, lds = (None, 0) if sum_out is None else _rows("sum_out", sum_out, (M, K), torch.float32)
+    pq = _dense("q", q, (M, K), torch.int8, torch.float8_e4m3fn)
+    ps = _dense("s", s, (M, blocks128(K)) if q.dtype == torch.float8_e4m3fn else (M,), torch.float32)
+    pw = _dense("norm_w", norm_w, (K,), torch.float32)
+    _check(load().fm_add_norm_quant(px, _DTYPES[x.dtype], ldx, pr, ldr, M, K, pw, eps,
+                                    _DTYPES[q.dtype], pq, ps, po, lds, _s(stream)))
+
+
+def prepare_linear_fp8(W, Wq, s_w, stream=None):
+    """W [N, K] fp32 -> e4m3 codes Wq [N, K] and s_w [blocks128(N), blocks128(K)]."""
+    N, K = W.shape
+    _check(load().fm_prepare_linear_fp8(
+        _dense("W", W, (N, K), torch.float32), N, K,
+        _dense("Wq", Wq, (N, K), torch.float8_e4m3fn),
+        _dense("s_w", s_w, (blocks128(N), blocks128(K)), torch.float32), _s(stream)))
+
+
+def fp8_gemm(A, s_a, W, s_w, Y, stream=None):
+    """Y [M, N] (fp32 or bf16, rows of any stride) = the block-scaled product of
+    the e4m3 codes A [M, K] and W [N, K]; s_a [M, blocks128(K)], s_w
+    [blocks128(N), blocks128(K)]."""
+    (M, K), N = A.shape, W.shape[0]
+    py, ldy = _rows("Y", Y, (M, N), torch.float32, torch.bfloat16)
+    kb = blocks128(K)
+    _check(load().fm_fp8_gemm(
+        _dense("A", A, (M, K), torch.float8_e4m3fn), _dense("s_a", s_a, (M, kb), torch.float32), M,
+        _dense("W", W, (N, K), torch.float8_e4m3fn),
+        _dense("s_w", s_w, (blocks128(N), kb), torch.float32), N, K, py, _DTYPES[Y.dtype], ldy,
+        _s(stream)))
+
+
+def embed_rows(ids, table, x, table_s=None, scale=1.0, stream=None):
+    """x [M, K] fp32 = scale * table[ids] for int32 ids (-1: zeros); table [V, K]
+    fp32, bf16, or e4m3 with table_s [blocks128(V), blocks128(K)]."""
+    (V, K), M = table.shape, ids.numel()
+    if (table.dtype == torch.float8_e4m3fn) != (table_s is not None):
+        raise ValueError("table_s: scales go with an e4m3 table, and only with one")
+    px, ldx = _rows("x", x, (M, K), torch.float32)
+    pt = _dense("table", table, (V, K), torch.float32, torch.bfloat16, torch.float8_e4m3fn)
+    pts = None if table_s is None else _dense("table_s", table_s, (blocks128(V), blocks128(K)),
+                                              torch.float32)
+    _check(load().fm_embed_rows(_dense("ids", ids, ids.shape, torch.int32), M, pt,
+                                _DTYPES[table.dtype], pts, V, K, scale, px, ldx, _s(stream)))
+
+
+def beam_workspace_bytes(B, beams, V, n_out) -> int:
+    return load().fm_beam_workspace_bytes(B, beams, V, n_out)
+
+
+def beam_select(logits, scores, out_scores, parent, token, ws, finished=None, out_finished=None,
+                eos=-1, stream=None):
+    """The n_out best (beam, token) pairs of each batch entry: logits
+    [B, beams, V] fp32 or bf16 (rows of any stride), scores [B, beams]; out_scores,
+    parent (int32) and token (int32) [B, n_out]; finished / out_finished uint8."""
+    B, beams, V = logits.shape
+    n = out_scores.shape[-1]
+    pl = _want("logits", logits, (B, beams, V), torch.float32, torch.bfloat16)
+    ld = logits.stride(1) if beams > 1 else logits.stride(0) if B > 1 else V
+    if (logits.stride(2) != 1 and V > 1) or (B > 1 and beams > 1 and logits.stride(0) != beams * ld):
+        raise ValueError("logits: rows [B * beams] of one stride and unit column stride are required")
+    pf = None if finished is None else _dense("finished", finished, (B, beams), torch.uint8)
+    po = None if out_finished is None else _dense("out_finished", out_finished, (B, n), torch.uint8)
+    _check(load().fm_beam_select(
+        pl, _DTYPES[logits.dtype], ld, B, beams, V,
+        _dense("scores", scores, (B, beams), torch.float32), pf, eos, n,
+        _dense("out_scores", out_scores, (B, n), torch.float32),
+        _dense("parent", parent, (B, n), torch.int32), _dense("token", token, (B, n), torch.int32),
+        po, _dense("ws", ws, ws.shape, ws.dtype), _nbytes(ws), _s(stream)))
+
+
+class RowSet:
+    """Buffers whose rows follow the beams (reorder_rows): dst tensors
+    [B * beams, ...], and src tensors of the same rows where they are not
+    reordered in place.  Holds the tensors and the pointer arrays of the call."""
+
+    def __init__(self, dst, src=None):
+        self.dst, self.src = list(dst), list(dst if src is None else src)
+        if len(self.dst) != len(self.src):
+            raise ValueError("RowSet: as many src as dst tensors are required")
+        for d, s in zip(self.dst, self.src):
+            _dense("dst", d, d.shape, d.dtype)
+            _dense("src", s, (s.shape[0],) + tuple(d.shape[1:]), d.dtype)
+        n = len(self.dst)
+        if n and len({(d.shape[0], s.shape[0]) for d, s in zip(self.dst, self.src)}) != 1:
+            raise ValueError("RowSet: every buffer must have the same number of rows")
+        self.dst_rows, self.src_rows = (self.dst[0].shape[0], self.src[0].shape[0]) if n else (0, 0)
+        self._dst = (C.c_void_p * n)(*[t.data_ptr() for t in self.dst])
+        self._src = (C.c_void_p * n)(*[t.data_ptr() for t in self.src])
+        self._row_bytes = (C.c_int64 * n)(
+            *[t.numel() // t.shape[0] * t.element_size() if t.shape[0] else 0 for t in self.dst])
+
+
+def reorder_rows(rows: RowSet, parent, src_beams=None, stream=None):
+    """dst[b, j] = src[b, parent[b, j]] for every buffer of the set; parent
+    [B, beams] int32.  src_beams: beams per batch entry of src (default: as dst)."""
+    B, beams = parent.shape
+    sb = beams if src_beams is None else src_beams
+    if rows.dst and (rows.dst_rows != B * beams or rows.src_rows != B * sb):
+        raise ValueError(f"reorder_rows: {rows.dst_rows} and {rows.src_rows} rows, expected "
+                         f"{B * beams} and {B * sb}")
+    _check(load().fm_reorder_rows(rows._src, rows._dst, rows._row_bytes, len(rows.dst), B, sb, beams,
+                                  _dense("parent", parent, (B, beams), torch.int32), _s(stream)))

@@ -137,7 +137,8 @@ class DeviceLayer:
 
 
 class DeviceStack:
-    """A stack of pre-normed residual mixer layers (no embedding / LM head)."""
+    """A stack of pre-normed residual mixer layers (DeviceLM adds the embedding
+    and the output head)."""
 
     def __init__(self, layer_params: list, shape: MixerShape, rotate=1, mode=lib.FM_DYNAMIC,
                  device="cuda"):
@@ -185,3 +186,122 @@ class DeviceStack:
         lib.stack_prefill_host([L.struct for L in self.layers], x_host, out_host, x_dev, B, T,
                                states, n_chunks, ws, stream)
         return out_host
+
+
+class DeviceLM:
+    """Token ids in, next tokens out: an embedding table, a DeviceStack, the final
+    RMSNorm and an output head, with beam search over the stack's carried states.
+
+    embedding [V, d_model] (fp32) is held as e4m3 codes with a scale per
+    128 x 128 block; head [V, d_model] likewise, or None where the output head
+    is tied to the embedding (one copy then serves both).  norm_w [d_model]:
+    the final norm's weight.  embed_scale multiplies the embedding rows."""
+
+    def __init__(self, layer_params: list, shape: MixerShape, embedding, norm_w, head=None,
+                 embed_scale: float = 1.0, rotate=1, mode=lib.FM_DYNAMIC, device="cuda"):
+        self.shape, self.embed_scale, self.device = shape, embed_scale, torch.device(device)
+        self.stack = DeviceStack(layer_params, shape, rotate, mode, device)
+        if not self.stack.layers:
+            raise ValueError("DeviceLM: at least one layer is required")
+        self.table, self.table_s = self._prepare(embedding)
+        self.head, self.head_s = ((self.table, self.table_s) if head is None
+                                  else self._prepare(head))
+        self.norm_w = _dev(norm_w, torch.float32, self.device)
+
+    def _prepare(self, w):
+        w = _dev(w, torch.float32, self.device)
+        if w.dim() != 2 or w.shape[1] != self.shape.d_model:
+            raise ValueError(f"DeviceLM: a [V, {self.shape.d_model}] matrix is required")
+        q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=self.device)
+        s = torch.empty(lib.blocks128(w.shape[0]), lib.blocks128(w.shape[1]), device=self.device)
+        lib.prepare_linear_fp8(w, q, s)
+        return q, s
+
+    def embed(self, ids: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+        """Rows [*ids.shape, d_model] of int32 token ids (-1: zeros)."""
+        d = self.shape.d_model
+        out = torch.empty(*ids.shape, d, device=self.device) if out is None else out
+        lib.embed_rows(ids, self.table, out.view(-1, d), self.table_s, self.embed_scale, stream)
+        return out
+
+    def calibrate(self, ids: torch.Tensor):
+        self.stack.calibrate(self.embed(ids))
+
+    def new_states(self, rows: int) -> list:
+        return [L.new_states(rows) for L in self.stack.layers]
+
+    def head_buffers(self, rows: int):
+        """(codes, scales, logits) for `rows` rows of logits()."""
+        d, V = self.shape.d_model, self.head.shape[0]
+        return (torch.empty(rows, d, dtype=torch.float8_e4m3fn, device=self.device),
+                torch.empty(rows, lib.blocks128(d), device=self.device),
+                torch.empty(rows, V, device=self.device))
+
+    def logits(self, h: torch.Tensor, residual=None, bufs=None, stream=None) -> torch.Tensor:
+        """Logits [rows, V] (fp32) of the rows h (+ residual), [rows, d_model]."""
+        q, s, y = self.head_buffers(h.shape[0]) if bufs is None else bufs
+        lib.add_norm_quant(h, self.norm_w, q, s, residual=residual, stream=stream)
+        lib.fp8_gemm(q, s, self.head, self.head_s, y, stream)
+        return y
+
+    def prefill(self, ids: torch.Tensor, states=None, stream=None) -> torch.Tensor:
+        """Logits [B, V] of the token after ids [B, T]; states are carried."""
+        x = self.embed(ids, stream=stream)
+        B, T, _ = x.shape
+        ws = self.stack.layers[0].workspace(B, T)
+        h = torch.empty_like(x)
+        last = len(self.stack.layers) - 1
+        for i, L in enumerate(self.stack.layers):
+            cs, ss = states[i] if states is not None else (None, None)
+            # the last layer's residual addition is the norm's
+            L.prefill(x, residual=i < last, conv_state=cs, ssm_state=ss,
+                      out=x if i < last else h, ws=ws, stream=stream)
+        return self.logits(h[:, -1], residual=x[:, -1], stream=stream)
+
+    def decode(self, ids: torch.Tensor, states: list, x=None, h=None, ws=None, bufs=None,
+               stream=None) -> torch.Tensor:
+        """Logits [rows, V] after one more token ids [rows]; states are updated.
+        x, h [rows, d_model], ws and bufs (head_buffers) may be kept by the caller."""
+        rows = ids.numel()
+        x = self.embed(ids, out=x, stream=stream)
+        h = torch.empty_like(x) if h is None else h
+        ws = self.stack.layers[0].workspace(rows, 1) if ws is None else ws
+        last = len(self.stack.layers) - 1
+        for i, L in enumerate(self.stack.layers):
+            L.decode(x, *states[i], residual=i < last, out=x if i < last else h, ws=ws,
+                     stream=stream)
+        return self.logits(h, residual=x, bufs=bufs, stream=stream)
+
+    def beam_search(self, ids: torch.Tensor, beams: int, steps: int, eos: int = -1):
+        """`steps` tokens after ids [B, T] (int32): tokens [B, beams, steps] (int32)
+        and scores [B, beams] (fp32 sums of log probabilities), best first.  A
+        beam that has ended goes on with eos; beams = 1 is greedy decoding.  Runs
+        on the current stream without synchronising it."""
+        if steps < 1:
+            raise ValueError("beam_search: steps must be positive")
+        B, V, d, dev = ids.shape[0], self.head.shape[0], self.shape.d_model, self.device
+        rows, i32 = B * beams, torch.int32
+        first = self.new_states(B)
+        y = self.prefill(ids, first)
+        scores = torch.zeros(B, 1, device=dev)
+        out = torch.empty(B, beams, device=dev)
+        parent, token = (torch.empty(B, beams, dtype=i32, device=dev) for _ in range(2))
+        fin = torch.empty(B, beams, dtype=torch.uint8, device=dev) if eos >= 0 else None
+        ws = torch.empty(max(lib.beam_workspace_bytes(B, k, V, beams) for k in (1, beams)),
+                         dtype=torch.uint8, device=dev)
+        lib.beam_select(y.view(B, 1, V), scores, out, parent, token, ws, out_finished=fin, eos=eos)
+        states = self.new_states(rows)
+        flat = lambda st: [t for pair in st for t in pair]
+        lib.reorder_rows(lib.RowSet(flat(states), flat(first)), parent, src_beams=1)
+        history = torch.full((rows, steps), -1, dtype=i32, device=dev)
+        history[:, 0] = token.view(-1)
+        kept = lib.RowSet(flat(states) + [history])
+        x, h = (torch.empty(rows, d, device=dev) for _ in range(2))
+        lws, bufs = self.stack.layers[0].workspace(rows, 1), self.head_buffers(rows)
+        for t in range(1, steps):
+            y = self.decode(token.view(-1), states, x, h, lws, bufs)
+            lib.beam_select(y.view(B, beams, V), out, out, parent, token, ws, finished=fin,
+                            out_finished=fin, eos=eos)
+            lib.reorder_rows(kept, parent)
+            history[:, t] = token.view(-1)
+        return history.view(B, beams, steps), out

@@ -1,0 +1,163 @@
+"""Host-side checks of the token loop's entry points that need no GPU: argument
+validation before any launch, workspace sizes, and the plain 64-bit forms the
+GPU tests compare against, each against its formula in another form."""
+import ctypes as C
+import math
+
+import pytest
+
+from quantized_state_space_mamba2_b200 import build as B
+
+torch = pytest.importorskip("torch")
+import token_plain as P  # noqa: E402
+
+p = [C.c_void_p(0x100000 * (i + 1)) for i in range(12)]  # aligned, never dereferenced
+odd = C.c_void_p(0x100004)
+OK, ARG, SHAPE, ALIGN, WS = 0, 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def so():
+    B.build()
+    from quantized_state_space_mamba2_b200 import lib
+    return lib.load()
+
+
+def test_status_name(so):
+    assert so.fm_status_string(9) == b"FM_ERR_INDEX"
+
+
+def norm(so, x=p[0], xt=0, ldx=256, res=p[1], ldr=256, M=4, K=256, w=p[2], eps=1e-5, qt=2, q=p[3],
+         s=p[4], out=p[5], lds=256):
+    return so.fm_add_norm_quant(x, xt, ldx, res, ldr, M, K, w, eps, qt, q, s, out, lds, None)
+
+
+def test_norm_refusals(so):
+    for bad in (dict(xt=2), dict(xt=3), dict(qt=0), dict(qt=1), dict(x=None), dict(w=None), dict(q=None),
+                dict(s=None), dict(eps=-1.0), dict(eps=0.0), dict(eps=math.nan), dict(eps=math.inf)):
+        assert norm(so, **bad) == ARG, bad
+    for bad in (dict(K=0), dict(K=250), dict(K=16400, ldx=16400, ldr=16400, lds=16400), dict(M=-1),
+                dict(M=1 << 31), dict(ldx=255), dict(ldx=258), dict(ldr=240), dict(lds=257)):
+        assert norm(so, **bad) == SHAPE, bad
+    for bad in (dict(x=odd), dict(res=odd), dict(w=odd), dict(q=odd), dict(s=odd), dict(out=odd)):
+        assert norm(so, **bad) == ALIGN, bad
+    assert norm(so, M=0, x=None) == OK
+
+
+def test_prepare_and_product_refusals(so):
+    assert so.fm_prepare_linear_fp8(None, 4, 32, p[0], p[1], None) == ARG
+    assert so.fm_prepare_linear_fp8(p[0], 4, 40, p[1], p[2], None) == SHAPE
+    assert so.fm_prepare_linear_fp8(p[0], 0, 32, p[1], p[2], None) == SHAPE
+    assert so.fm_prepare_linear_fp8(odd, 4, 32, p[1], p[2], None) == ALIGN
+
+    def gemm(A=p[0], sa=p[1], M=4, W=p[2], sw=p[3], N=100, K=256, Y=p[4], yt=0, ldy=100):
+        return so.fm_fp8_gemm(A, sa, M, W, sw, N, K, Y, yt, ldy, None)
+
+    for bad in (dict(A=None), dict(sa=None), dict(W=None), dict(sw=None), dict(Y=None), dict(yt=2),
+                dict(yt=3), dict(yt=9)):
+        assert gemm(**bad) == ARG, bad
+    for bad in (dict(K=0), dict(K=-16), dict(K=100), dict(ldy=99), dict(M=-1), dict(N=-1), dict(M=1 << 40),
+                dict(N=1 << 40, ldy=1 << 40)):
+        assert gemm(**bad) == SHAPE, bad
+    for bad in (dict(A=odd), dict(sa=odd), dict(W=odd), dict(sw=odd), dict(Y=odd)):
+        assert gemm(**bad) == ALIGN, bad
+    assert gemm(M=0, A=None) == OK and gemm(N=0, ldy=0, W=None) == OK
+
+
+def test_embed_refusals(so):
+    def emb(ids=p[0], M=4, t=p[1], tt=0, ts=None, V=100, K=256, x=p[2], ldx=256):
+        return so.fm_embed_rows(ids, M, t, tt, ts, V, K, 1.0, x, ldx, None)
+
+    for bad in (dict(ids=None), dict(t=None), dict(x=None), dict(tt=3), dict(tt=2)):  # e4m3 needs scales
+        assert emb(**bad) == ARG, bad
+    for bad in (dict(V=0), dict(V=1 << 31), dict(K=8), dict(K=0), dict(ldx=255), dict(ldx=257), dict(M=-1)):
+        assert emb(**bad) == SHAPE, bad
+    assert emb(x=odd) == ALIGN and emb(ids=odd) == ALIGN
+    assert emb(M=0, ids=None) == OK
+
+
+def test_beam_refusals_and_workspace(so):
+    from quantized_state_space_mamba2_b200 import lib
+    need = lib.beam_workspace_bytes(2, 4, 1000, 4)
+    assert need > 0 and lib.beam_workspace_bytes(0, 4, 1000, 4) >= 0
+    for bad in ((2, 33, 1000, 4), (2, 0, 1000, 4), (2, 4, 0, 4), (2, 4, 1 << 31, 4), (2, 4, 1000, 33),
+                (2, 4, 1000, 0), (-1, 4, 1000, 4)):
+        assert lib.beam_workspace_bytes(*bad) == 0, bad
+
+    def sel(l=p[0], t=0, ld=1000, B=2, k=4, V=1000, sc=p[1], fin=None, eos=-1, n=4, o=p[2], par=p[3],
+            tok=p[4], of=None, ws=p[5], nb=need):
+        return so.fm_beam_select(l, t, ld, B, k, V, sc, fin, eos, n, o, par, tok, of, ws, nb, None)
+
+    for bad in (dict(l=None), dict(t=2), dict(sc=None), dict(o=None), dict(par=None), dict(tok=None),
+                dict(fin=p[6]), dict(eos=1000), dict(eos=-2), dict(o=p[1], n=3),
+                dict(fin=p[6], of=p[6], eos=1, n=3)):
+        assert sel(**bad) == ARG, bad
+    for bad in (dict(k=33), dict(n=33), dict(n=0), dict(V=0), dict(ld=999), dict(B=-1)):
+        assert sel(**bad) == SHAPE, bad
+    for bad in (dict(l=odd), dict(sc=odd), dict(o=odd), dict(ws=odd)):
+        assert sel(**bad) == ALIGN, bad
+    assert sel(ws=None) == WS and sel(nb=need - 1) == WS
+    assert sel(B=0, l=None) == OK
+
+
+def test_reorder_refusals(so):
+    def arr(*v):
+        return (C.c_void_p * len(v))(*v)
+
+    nb = (C.c_int64 * 2)(64, 128)
+
+    def ro(src=arr(0x100000, 0x200000), dst=arr(0x100000, 0x200000), nbytes=nb, n=2, B=2, sb=4, db=4,
+           par=p[9]):
+        return so.fm_reorder_rows(src, dst, nbytes, n, B, sb, db, par, None)
+
+    for bad in (dict(n=-1), dict(src=None), dict(dst=None), dict(nbytes=None), dict(par=None),
+                dict(src=arr(0, 0x200000)), dict(sb=1),  # in place needs as many beams
+                dict(src=arr(0x100000 + 16, 0x200000))):  # overlapping, not the same
+        assert ro(**bad) == ARG, bad
+    for bad in (dict(B=-1), dict(B=65536), dict(sb=33, db=33), dict(db=0), dict(nbytes=(C.c_int64 * 2)(64, -1))):
+        assert ro(**bad) == SHAPE, bad
+    assert ro(src=arr(0x100000, 0x200004), dst=arr(0x300000, 0x400000)) == ALIGN
+    assert ro(n=0, src=None) == OK and ro(B=0) == OK
+
+
+def test_python_checks():
+    """The binding refuses what the library could not see: types, shapes, devices."""
+    from quantized_state_space_mamba2_b200 import lib
+    z = torch.zeros
+    with pytest.raises(ValueError, match="CUDA"):
+        lib.add_norm_quant(z(2, 32), z(32), z(2, 32, dtype=torch.int8), z(2))
+    with pytest.raises(ValueError, match="dtype"):
+        lib.add_norm_quant(z(2, 32, dtype=torch.float16), z(32), z(2, 32, dtype=torch.int8), z(2))
+    with pytest.raises(ValueError, match="shape"):
+        lib.fp8_gemm(z(2, 32), z(2, 1), z(3, 32), z(1, 1), z(2, 4))
+    with pytest.raises(ValueError, match="scales"):
+        lib.embed_rows(z(2, dtype=torch.int32), z(4, 16), z(2, 16), table_s=z(1, 1))
+
+
+# ------------------------------------------------------------------ the plain forms
+def test_plain_e4m3_is_the_types_rounding():
+    v = torch.randn(20000, generator=torch.Generator().manual_seed(1)) * torch.logspace(-4, 3, 20000)
+    want = v.clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    assert torch.equal(P.e4m3_round(v.double()).float(), want)
+
+
+def test_plain_norm_and_product():
+    g = torch.Generator().manual_seed(2)
+    x, w = torch.randn(5, 400, generator=g), torch.ones(400)
+    r, codes, s, sure = P.norm(x, x, w, 1e-5, "e4m3")
+    assert torch.equal(r, x + x) and bool((sure == 1).all())
+    y = torch.nn.functional.rms_norm((x + x).double(), (400,), eps=1e-5)
+    assert float((P.dequant_rows(codes, s) - y).abs().max()) <= float(y.abs().max()) * 2.0 ** -4
+    _, c8, s8, _ = P.norm(x, None, w, 1e-5, "int8")
+    y = torch.nn.functional.rms_norm(x.double(), (400,), eps=1e-5)
+    assert bool(((c8 * s8[:, None] - y).abs() <= 0.5001 * s8[:, None]).all())
+
+
+def test_plain_beam_is_a_sort_of_all_candidates():
+    g = torch.Generator().manual_seed(3)
+    l, sc = torch.randn(3, 4, 50, generator=g) * 2, -torch.rand(3, 4, generator=g)
+    out, par, tok, _ = P.beam(l, sc, None, -1, 7)
+    c = torch.log_softmax(l.double(), 2) + sc.double()[:, :, None]
+    v, i = torch.sort(c.view(3, -1), dim=1, descending=True, stable=True)
+    assert torch.allclose(out, v[:, :7], rtol=0, atol=1e-12)
+    assert torch.equal(par * 50 + tok, i[:, :7])
