@@ -59,33 +59,105 @@ extern "C" fm_status fm_prepare_linear_fp8(const float *W, int64_t N, int64_t K,
   return launched("k_prepare_linear_fp8");
 }
 
+// Output map of the large kernel's TMA stores: N columns, rows ldy elements
+// apart, boxes of 32 rows x 128 bytes in the staging buffers' 128-byte swizzle.
+static fm_status make_tmap_rows(CUtensorMap *tm, void *Y, bool f32, long long N, long long M,
+                                long long ldy) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(FM_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled entry point unavailable");
+  const cuuint32_t es = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+  cuuint64_t strides[1] = {(cuuint64_t)ldy * es};
+  cuuint32_t box[2] = {128 / es, 32};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y,
+                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FM_ERR_CUDA, "cuTensorMapEncodeTiled (output) failed (%d)", (int)r);
+  return FM_OK;
+}
+
+template <int BN, int STAGES, typename TY>
+static fm_status launch_fp8_large(const void *A, const void *W, long long K, Fp8Args a,
+                                  cudaStream_t st) {
+  using Sm = Fp8Smem<BN, STAGES>;
+  static_assert(Sm::kBytes <= 227 * 1024, "shared memory per CTA");
+  CUtensorMap ta, tb, ty;
+  FM_TRY(make_tmap(&ta, (const int8_t *)A, a.M, K, kGemmBM));
+  FM_TRY(make_tmap(&tb, (const int8_t *)W, a.N, K, BN));
+  ty = ta;
+  // the TMA unit clips rows in units of 16 bytes: a row that ends inside one
+  // would have what lies behind it overwritten
+  a.tma_store = a.ldy * (long long)sizeof(TY) % 16 == 0 && a.N * (long long)sizeof(TY) % 16 == 0;
+  if (a.tma_store) FM_TRY(make_tmap_rows(&ty, a.Y, sizeof(TY) == 4, a.N, a.M, a.ldy));
+  const long long mt = (a.M + kGemmBM - 1) / kGemmBM, nt = (a.N + BN - 1) / BN;
+  if (mt * nt > 0x7FFFFFFF) return fail(FM_ERR_SHAPE, "fm_fp8_gemm: too many output tiles");
+  a.m_tiles = (int)mt;
+  a.n_tiles = (int)nt;
+  auto kern = k_fp8_gemm_tc<BN, STAGES, TY>;
+  FM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes));
+  const unsigned grid = (unsigned)(mt * nt < sm_count() ? mt * nt : sm_count());
+  FM_TRY(launch_ex("k_fp8_gemm_tc", kern, grid, kFp8Threads, Sm::kBytes, st, ta, tb, ty, a));
+  return launched("k_fp8_gemm_tc");
+}
+
+template <int MP, int STAGES, typename TY>
+static fm_status launch_fp8_small(const void *A, const void *W, long long K, Fp8Args a,
+                                  cudaStream_t st) {
+  using Sm = Fp8SmallSmem<MP, STAGES>;
+  static_assert(Sm::kBytes <= 227 * 1024, "shared memory per CTA");
+  CUtensorMap ta, tw;
+  FM_TRY(make_tmap(&ta, (const int8_t *)A, a.M, K, MP));
+  FM_TRY(make_tmap(&tw, (const int8_t *)W, a.N, K, kGemmBM));
+  a.n_tiles = (int)((a.N + kGemmBM - 1) / kGemmBM);
+  auto kern = k_fp8_gemm_small<MP, STAGES, TY>;
+  FM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes));
+  const unsigned grid = (unsigned)(a.n_tiles < sm_count() ? a.n_tiles : sm_count());
+  FM_TRY(launch_ex("k_fp8_gemm_small", kern, grid, 64 + 32 * Sm::kEpi, Sm::kBytes, st, tw, ta, a));
+  return launched("k_fp8_gemm_small");
+}
+
+template <typename TY>
+static fm_status launch_fp8(const void *A, const void *W, long long K, const Fp8Args &a,
+                            cudaStream_t st) {
+  if (a.M <= 16) return launch_fp8_small<16, 11, TY>(A, W, K, a, st);
+  if (a.M <= 32) return launch_fp8_small<32, 10, TY>(A, W, K, a, st);
+  if (a.M <= 64) return launch_fp8_small<64, 9, TY>(A, W, K, a, st);
+  if (a.M <= 128) return launch_fp8_small<128, 6, TY>(A, W, K, a, st);
+  // 256 columns per tile halve the traffic of A; narrower tiles where those
+  // would leave SMs idle
+  if ((a.M + kGemmBM - 1) / kGemmBM * ((a.N + 255) / 256) >= sm_count())
+    return launch_fp8_large<256, 4, TY>(A, W, K, a, st);
+  return launch_fp8_large<128, 6, TY>(A, W, K, a, st);
+}
+
 extern "C" fm_status fm_fp8_gemm(const void *A, const float *s_a, int64_t M, const void *W,
                                  const float *s_w, int64_t N, int64_t K, void *Y, fm_dtype y_type,
                                  int64_t ldy, fm_stream stream) {
   if (y_type != FM_F32 && y_type != FM_BF16)
     return fail(FM_ERR_INVALID_ARG, "%s: Y must be fp32 or bf16", __func__);
-  if (M < 0 || N < 0 || M > 65535 * 64 || N > 0x7FFFFFFF || K <= 0 || K % 16 || K > 0x7FFFFFFF)
-    return fail(FM_ERR_SHAPE,
-                "%s: need 0 <= M <= 65535 * 64, 0 <= N < 2^31 and K a positive multiple of 16",
+  if (M < 0 || N < 0 || M > 0x7FFFFF00 || N > 0x7FFFFF00 || K <= 0 || K % 16 || K > 0x7FFFFF00)
+    return fail(FM_ERR_SHAPE, "%s: need M, N, K <= 2^31 - 256, M, N >= 0 and K a positive multiple of 16",
                 __func__);
-  if (ldy < N) return fail(FM_ERR_SHAPE, "%s: ldy is less than N", __func__);
+  if (ldy < N || ldy > (int64_t)1 << 36)
+    return fail(FM_ERR_SHAPE, "%s: ldy is less than N or above 2^36", __func__);
   if (M == 0 || N == 0) return FM_OK;
   NEED(A);
   NEED(s_a);
   NEED(W);
   NEED(s_w);
   NEED(Y);
-  const dim3 grid((unsigned)((N + 63) / 64), (unsigned)((M + 63) / 64));
-  if (y_type == FM_F32)
-    FM_TRY(launch_ex("k_fp8_gemm", k_fp8_gemm_simple<float>, grid, 256, 0, (cudaStream_t)stream,
-                     (const uint8_t *)A, s_a, (long long)M, (const uint8_t *)W, s_w, (long long)N,
-                     (int)K, (float *)Y, (long long)ldy));
-  else
-    FM_TRY(launch_ex("k_fp8_gemm", k_fp8_gemm_simple<__nv_bfloat16>, grid, 256, 0,
-                     (cudaStream_t)stream, (const uint8_t *)A, s_a, (long long)M,
-                     (const uint8_t *)W, s_w, (long long)N, (int)K, (__nv_bfloat16 *)Y,
-                     (long long)ldy));
-  return launched("k_fp8_gemm");
+  Fp8Args a = {};
+  a.s_a = s_a;
+  a.s_w = s_w;
+  a.M = M;
+  a.N = N;
+  a.ldy = ldy;
+  a.Y = Y;
+  a.nkb = (int)((K + kGemmBK - 1) / kGemmBK);
+  return y_type == FM_F32 ? launch_fp8<float>(A, W, K, a, (cudaStream_t)stream)
+                          : launch_fp8<__nv_bfloat16>(A, W, K, a, (cudaStream_t)stream);
 }
 
 // ------------------------------------------------------------------ beam selection
