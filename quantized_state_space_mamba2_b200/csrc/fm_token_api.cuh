@@ -96,6 +96,14 @@ static fm_status launch_fp8_large(const void *A, const void *W, long long K, Fp8
   a.m_tiles = (int)mt;
   a.n_tiles = (int)nt;
   auto kern = k_fp8_gemm_tc<BN, STAGES, TY>;
+  // the warpgroups' register shares must fit what the block is launched with
+  // (a share that does not would wait for ever)
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, k_fp8_gemm_tc<BN, STAGES, TY>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs * kFp8Threads < 128 * kFp8RegsLoad + (kFp8Threads - 128) * kFp8RegsAcc)
+    return fail(FM_ERR_UNSUPPORTED, "k_fp8_gemm_tc: built with %d registers per thread", regs);
   FM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes));
   const unsigned grid = (unsigned)(mt * nt < sm_count() ? mt * nt : sm_count());
   FM_TRY(launch_ex("k_fp8_gemm_tc", kern, grid, kFp8Threads, Sm::kBytes, st, ta, tb, ty, a));

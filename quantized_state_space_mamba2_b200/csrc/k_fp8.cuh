@@ -55,6 +55,17 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
                : "memory");
   asm volatile("" : "+r"(r[30]), "+r"(r[31]));
 }
+// the same for values of a load that the wait just above has completed
+__device__ __forceinline__ void tmem_ld_tie(uint32_t (&r)[32]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+  asm volatile(""
+               : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
 // acc (two fp32) += (lo, hi) * c (two fp32), each a single rounding
 __device__ __forceinline__ void ffma2(unsigned long long &acc, uint32_t lo, uint32_t hi,
                                       unsigned long long c) {
@@ -76,10 +87,14 @@ struct Fp8Args {
 
 // ------------------------------------------------------------ large M
 // One CTA per SM walks 128 x BN output tiles.  Warp 0 loads (TMA, a ring of
-// STAGES 128-deep blocks), one lane of warp 1 issues the MMAs, warps 2..9 hold
+// STAGES 128-deep blocks), one lane of warp 1 issues the MMAs, warps 4..11 hold
 // the fp32 accumulators: warp w the 32 rows of TMEM lane quarter w % 4 (lane =
 // row) and one half of the tile's columns, so s_a s_w is one number per thread
-// and block.
+// and block.  128 accumulators and 64 values on their way from TMEM need more
+// registers than an even share: the first warpgroup hands its own over.
+// A TMEM load takes about 115 cycles and another one behind it 16 more
+// (measured), so 64 columns are loaded per wait and the two warps of a
+// scheduler cover each other's wait.
 template <int BN, int STAGES>
 struct Fp8Smem {
   static constexpr int kA = kGemmBM * kGemmBK, kB = BN * kGemmBK;
@@ -88,7 +103,9 @@ struct Fp8Smem {
   static constexpr int kBytes = 1024 + STAGES * (kA + kB) + 8 * kStage +
                                 (2 * STAGES + 2 * kAcc + 1) * 8 + 16;
 };
-constexpr int kFp8Threads = 320;
+constexpr int kFp8Threads = 384;
+// registers per thread of the first warpgroup and of the two others
+constexpr int kFp8RegsLoad = 40, kFp8RegsAcc = 224;
 
 // The 32 x 32 (fp32) or 32 x 64 (bf16) chunk of the tile at (row0, col0), from
 // the lanes' rows (lane = row), 128 bytes each, through the warp's staging
@@ -178,56 +195,60 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 0) {
-    if (lane == 0) {
-      bool ok = !(g_test_stall & kStallGemm);
-      long long it = 0;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-        const int m0 = (t / a.n_tiles) * kGemmBM, n0 = (t % a.n_tiles) * BN;
-        for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-          const int s = (int)(it % STAGES);
-          if (!mbar_wait(&empty_bar[s], ((uint32_t)(it / STAGES) & 1u) ^ 1u)) {
-            ok = false;
-            break;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8RegsLoad));
+    if (warp == 0) {
+      if (lane == 0) {
+        bool ok = !(g_test_stall & kStallGemm);
+        long long it = 0;
+        for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+          const int m0 = (t / a.n_tiles) * kGemmBM, n0 = (t % a.n_tiles) * BN;
+          for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+            const int s = (int)(it % STAGES);
+            if (!mbar_wait(&empty_bar[s], ((uint32_t)(it / STAGES) & 1u) ^ 1u)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(Sm::kA + Sm::kB));
+            tma_load_2d(sA + s * Sm::kA, &tmA, kb * kGemmBK, m0, &full_bar[s]);
+            tma_load_2d(sB + s * Sm::kB, &tmB, kb * kGemmBK, n0, &full_bar[s]);
           }
-          mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(Sm::kA + Sm::kB));
-          tma_load_2d(sA + s * Sm::kA, &tmA, kb * kGemmBK, m0, &full_bar[s]);
-          tma_load_2d(sB + s * Sm::kB, &tmB, kb * kGemmBK, n0, &full_bar[s]);
         }
+        // every copy issued must have landed before the CTA may exit
+        for (long long j = it > STAGES ? it - STAGES : 0; j < it; ++j)
+          if (!mbar_drain(&full_bar[j % STAGES], (uint32_t)(j / STAGES) & 1u)) break;
       }
-      // every copy issued must have landed before the CTA may exit
-      for (long long j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-        if (!mbar_drain(&full_bar[j % STAGES], (uint32_t)(j / STAGES) & 1u)) break;
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = e4m3_idesc(kGemmBM, BN);
-      long long it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x)
-        for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-          const int s = (int)(it % STAGES), acc = (int)(it % kAcc);
-          if (!mbar_wait(&tempty[acc], ((uint32_t)(it / kAcc) & 1u) ^ 1u) ||
-              !mbar_wait(&full_bar[s], (uint32_t)(it / STAGES) & 1u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t ad = sw128_desc(smem_u32(sA + s * Sm::kA));
-          const uint64_t bd = sw128_desc(smem_u32(sB + s * Sm::kB));
+    } else if (warp == 1) {
+      if (lane == 0) {
+        constexpr uint32_t idesc = e4m3_idesc(kGemmBM, BN);
+        long long it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x)
+          for (int kb = 0; kb < a.nkb; ++kb, ++it) {
+            const int s = (int)(it % STAGES), acc = (int)(it % kAcc);
+            if (!mbar_wait(&tempty[acc], ((uint32_t)(it / kAcc) & 1u) ^ 1u) ||
+                !mbar_wait(&full_bar[s], (uint32_t)(it / STAGES) & 1u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = sw128_desc(smem_u32(sA + s * Sm::kA));
+            const uint64_t bd = sw128_desc(smem_u32(sB + s * Sm::kB));
 #pragma unroll
-          for (int k = 0; k < kGemmBK / 32; ++k)
-            mma_e4m3(tmem_base + (uint32_t)(acc * BN), ad + (uint64_t)(2 * k),
-                     bd + (uint64_t)(2 * k), idesc, k > 0 ? 1u : 0u);
-          mma_commit(&empty_bar[s]);
-          mma_commit(&tfull[acc]);
-        }
-      // wait for every MMA issued so far before TMEM can be released
-      mma_commit(drain_bar);
-      mbar_drain(drain_bar, 0);
+            for (int k = 0; k < kGemmBK / 32; ++k)
+              mma_e4m3(tmem_base + (uint32_t)(acc * BN), ad + (uint64_t)(2 * k),
+                       bd + (uint64_t)(2 * k), idesc, k > 0 ? 1u : 0u);
+            mma_commit(&empty_bar[s]);
+            mma_commit(&tfull[acc]);
+          }
+        // wait for every MMA issued so far before TMEM can be released
+        mma_commit(drain_bar);
+        mbar_drain(drain_bar, 0);
+      }
     }
   } else {
-    const int e = warp - 2, quarter = warp & 3, half = e / 4;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8RegsAcc));
+    const int e = warp - 4, quarter = warp & 3, half = e / 4;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kCols);
     long long it = 0;
     bool ok = true;
@@ -254,21 +275,22 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         if (!ok) break;
         tc_fence_after();
         const unsigned long long c2 = pack2(c, c);
-        uint32_t r[2][32];
-        tmem_ld32_issue(lane_base + (uint32_t)(buf * BN), r[0]);
 #pragma unroll
-        for (int q = 0; q < kCols / 32; ++q) {
-          tmem_ld_wait(r[q & 1]);
-          if (q + 1 < kCols / 32)
-            tmem_ld32_issue(lane_base + (uint32_t)(buf * BN + 32 * (q + 1)), r[(q + 1) & 1]);
-          else {  // the last load has completed: hand the buffer back
+        for (int q = 0; q < kCols; q += 64) {
+          uint32_t r0[32], r1[32];
+          tmem_ld32_issue(lane_base + (uint32_t)(buf * BN + q), r0);
+          tmem_ld32_issue(lane_base + (uint32_t)(buf * BN + q + 32), r1);
+          tmem_ld_wait(r0);
+          tmem_ld_tie(r1);
+          if (q + 64 == kCols) {  // the last load has completed: hand the buffer back
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[buf]);
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            ffma2(acc[16 * q + j], r[q & 1][2 * j], r[q & 1][2 * j + 1], c2);
+          for (int j = 0; j < 16; ++j) ffma2(acc[q / 2 + j], r0[2 * j], r0[2 * j + 1], c2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) ffma2(acc[q / 2 + 16 + j], r1[2 * j], r1[2 * j + 1], c2);
         }
       }
       if (!ok) break;

@@ -509,83 +509,103 @@ def blocks128(n: int) -> int:
     return (n + 127) // 128
 
 
-def _want(name, t, shape, *dtypes):
-    """A tensor argument's shape, type and device: a CUDA tensor on the current
-    device (the call launches there), rows of any stride, unit column stride."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _place(stream):
+    """(current device, raw stream) of a call: its tensors must be on that device,
+    where it is launched."""
+    dev = torch.cuda.current_device()
+    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _bad(name, t, shape, dtypes):
+    """Why _want or _dense refused a tensor."""
+    if t.shape != shape:
+        return ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: libfastmamba takes CUDA tensors on the current device")
-    return C.c_void_p(t.data_ptr())
+        return ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.device.type != "cuda" or t.get_device() != torch.cuda.current_device():
+        return ValueError(f"{name}: libfastmamba takes CUDA tensors on the current device")
+    return ValueError(f"{name}: a contiguous tensor is required")
 
 
-def _dense(name, t, shape, *dtypes):
-    p = _want(name, t, shape, *dtypes)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous tensor is required")
-    return p
+def _dense(name, t, shape, dtypes, dev):
+    """The address of a contiguous tensor argument of this shape, one of these
+    types and this device."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
+        raise _bad(name, t, shape, dtypes)
+    return t.data_ptr()
 
 
-def _rows(name, t, shape, *dtypes):
-    """(pointer, row stride in elements) of a matrix with unit column stride."""
-    p = _want(name, t, shape, *dtypes)
-    if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+def _rows(name, t, shape, dtypes, dev):
+    """(address, row stride in elements) of a matrix with unit column stride."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev:
+        raise _bad(name, t, shape, dtypes)
+    rs, cs = t.stride()
+    if cs != 1 and shape[1] > 1 and shape[0]:
         raise ValueError(f"{name}: unit column stride is required")
-    return p, t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+    return t.data_ptr(), rs if shape[0] > 1 else shape[1]
+
+
+_F32, _BF16, _FP8, _INT8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.int8
+_T_F32, _T_I32, _T_U8, _T_FP8 = (_F32,), (torch.int32,), (torch.uint8,), (_FP8,)
+_T_ROWS, _T_CODES, _T_TABLE = (_F32, _BF16), (_FP8, _INT8), (_F32, _BF16, _FP8)
 
 
 def add_norm_quant(x, norm_w, q, s, residual=None, sum_out=None, eps=1e-5, stream=None):
     """r = x + residual; RMSNorm(r) * norm_w as 8-bit codes.  q int8 [M, K] with
     s [M] (a scale per row), or float8_e4m3fn with s [M, blocks128(K)] (one per
     128 columns); sum_out (may be x or residual) receives r."""
-    M, K = x.shape
-    px, ldx = _rows("x", x, (M, K), torch.float32, torch.bfloat16)
-    pr, ldr = (None, 0) if residual is None else _rows("residual", residual, (M, K), torch.float32)
-    po, lds = (None, 0) if sum_out is None else _rows("sum_out", sum_out, (M, K), torch.float32)
-    pq = _dense("q", q, (M, K), torch.int8, torch.float8_e4m3fn)
-    ps = _dense("s", s, (M, blocks128(K)) if q.dtype == torch.float8_e4m3fn else (M,), torch.float32)
-    pw = _dense("norm_w", norm_w, (K,), torch.float32)
-    _check(load().fm_add_norm_quant(px, _DTYPES[x.dtype], ldx, pr, ldr, M, K, pw, eps,
-                                    _DTYPES[q.dtype], pq, ps, po, lds, _s(stream)))
+    dev, st = _place(stream)
+    M, K = mk = x.shape
+    px, ldx = _rows("x", x, mk, _T_ROWS, dev)
+    pr, ldr = (None, 0) if residual is None else _rows("residual", residual, mk, _T_F32, dev)
+    po, lds = (None, 0) if sum_out is None else _rows("sum_out", sum_out, mk, _T_F32, dev)
+    pq = _dense("q", q, mk, _T_CODES, dev)
+    ps = _dense("s", s, (M, (K + 127) // 128) if q.dtype is _FP8 else (M,), _T_F32, dev)
+    _check(load().fm_add_norm_quant(px, _DTYPES[x.dtype], ldx, pr, ldr, M, K,
+                                    _dense("norm_w", norm_w, (K,), _T_F32, dev), eps,
+                                    _DTYPES[q.dtype], pq, ps, po, lds, st))
 
 
 def prepare_linear_fp8(W, Wq, s_w, stream=None):
     """W [N, K] fp32 -> e4m3 codes Wq [N, K] and s_w [blocks128(N), blocks128(K)]."""
+    dev, st = _place(stream)
     N, K = W.shape
     _check(load().fm_prepare_linear_fp8(
-        _dense("W", W, (N, K), torch.float32), N, K,
-        _dense("Wq", Wq, (N, K), torch.float8_e4m3fn),
-        _dense("s_w", s_w, (blocks128(N), blocks128(K)), torch.float32), _s(stream)))
+        _dense("W", W, (N, K), _T_F32, dev), N, K, _dense("Wq", Wq, (N, K), _T_FP8, dev),
+        _dense("s_w", s_w, (blocks128(N), blocks128(K)), _T_F32, dev), st))
 
 
 def fp8_gemm(A, s_a, W, s_w, Y, stream=None):
     """Y [M, N] (fp32 or bf16, rows of any stride) = the block-scaled product of
     the e4m3 codes A [M, K] and W [N, K]; s_a [M, blocks128(K)], s_w
     [blocks128(N), blocks128(K)]."""
+    dev, st = _place(stream)
     (M, K), N = A.shape, W.shape[0]
-    py, ldy = _rows("Y", Y, (M, N), torch.float32, torch.bfloat16)
-    kb = blocks128(K)
+    py, ldy = _rows("Y", Y, (M, N), _T_ROWS, dev)
+    kb = (K + 127) // 128
     _check(load().fm_fp8_gemm(
-        _dense("A", A, (M, K), torch.float8_e4m3fn), _dense("s_a", s_a, (M, kb), torch.float32), M,
-        _dense("W", W, (N, K), torch.float8_e4m3fn),
-        _dense("s_w", s_w, (blocks128(N), kb), torch.float32), N, K, py, _DTYPES[Y.dtype], ldy,
-        _s(stream)))
+        _dense("A", A, (M, K), _T_FP8, dev), _dense("s_a", s_a, (M, kb), _T_F32, dev), M,
+        _dense("W", W, (N, K), _T_FP8, dev),
+        _dense("s_w", s_w, ((N + 127) // 128, kb), _T_F32, dev), N, K, py, _DTYPES[Y.dtype], ldy, st))
 
 
 def embed_rows(ids, table, x, table_s=None, scale=1.0, stream=None):
     """x [M, K] fp32 = scale * table[ids] for int32 ids (-1: zeros); table [V, K]
     fp32, bf16, or e4m3 with table_s [blocks128(V), blocks128(K)]."""
-    (V, K), M = table.shape, ids.numel()
-    if (table.dtype == torch.float8_e4m3fn) != (table_s is not None):
+    if (table.dtype is _FP8) != (table_s is not None):
         raise ValueError("table_s: scales go with an e4m3 table, and only with one")
-    px, ldx = _rows("x", x, (M, K), torch.float32)
-    pt = _dense("table", table, (V, K), torch.float32, torch.bfloat16, torch.float8_e4m3fn)
-    pts = None if table_s is None else _dense("table_s", table_s, (blocks128(V), blocks128(K)),
-                                              torch.float32)
-    _check(load().fm_embed_rows(_dense("ids", ids, ids.shape, torch.int32), M, pt,
-                                _DTYPES[table.dtype], pts, V, K, scale, px, ldx, _s(stream)))
+    dev, st = _place(stream)
+    (V, K), M = table.shape, ids.numel()
+    px, ldx = _rows("x", x, (M, K), _T_F32, dev)
+    pts = None if table_s is None else _dense("table_s", table_s,
+                                              ((V + 127) // 128, (K + 127) // 128), _T_F32, dev)
+    _check(load().fm_embed_rows(_dense("ids", ids, ids.shape, _T_I32, dev), M,
+                                _dense("table", table, (V, K), _T_TABLE, dev),
+                                _DTYPES[table.dtype], pts, V, K, scale, px, ldx, st))
 
 
 def beam_workspace_bytes(B, beams, V, n_out) -> int:
@@ -597,20 +617,27 @@ def beam_select(logits, scores, out_scores, parent, token, ws, finished=None, ou
     """The n_out best (beam, token) pairs of each batch entry: logits
     [B, beams, V] fp32 or bf16 (rows of any stride), scores [B, beams]; out_scores,
     parent (int32) and token (int32) [B, n_out]; finished / out_finished uint8."""
+    dev, st = _place(stream)
     B, beams, V = logits.shape
     n = out_scores.shape[-1]
-    pl = _want("logits", logits, (B, beams, V), torch.float32, torch.bfloat16)
-    ld = logits.stride(1) if beams > 1 else logits.stride(0) if B > 1 else V
-    if (logits.stride(2) != 1 and V > 1) or (B > 1 and beams > 1 and logits.stride(0) != beams * ld):
+    if logits.dtype not in _T_ROWS or logits.get_device() != dev:
+        raise _bad("logits", logits, logits.shape, _T_ROWS)
+    sb, ld, sv = logits.stride()
+    if beams == 1:
+        ld = sb if B > 1 else V
+    if (sv != 1 and V > 1) or (B > 1 and sb != beams * ld):
         raise ValueError("logits: rows [B * beams] of one stride and unit column stride are required")
-    pf = None if finished is None else _dense("finished", finished, (B, beams), torch.uint8)
-    po = None if out_finished is None else _dense("out_finished", out_finished, (B, n), torch.uint8)
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise _bad("ws", ws, ws.shape, (ws.dtype,))
+    bk, bn = (B, beams), (B, n)
     _check(load().fm_beam_select(
-        pl, _DTYPES[logits.dtype], ld, B, beams, V,
-        _dense("scores", scores, (B, beams), torch.float32), pf, eos, n,
-        _dense("out_scores", out_scores, (B, n), torch.float32),
-        _dense("parent", parent, (B, n), torch.int32), _dense("token", token, (B, n), torch.int32),
-        po, _dense("ws", ws, ws.shape, ws.dtype), _nbytes(ws), _s(stream)))
+        logits.data_ptr(), _DTYPES[logits.dtype], ld, B, beams, V,
+        _dense("scores", scores, bk, _T_F32, dev),
+        None if finished is None else _dense("finished", finished, bk, _T_U8, dev), eos, n,
+        _dense("out_scores", out_scores, bn, _T_F32, dev),
+        _dense("parent", parent, bn, _T_I32, dev), _dense("token", token, bn, _T_I32, dev),
+        None if out_finished is None else _dense("out_finished", out_finished, bn, _T_U8, dev),
+        ws.data_ptr(), ws.numel() * ws.element_size(), st))
 
 
 class RowSet:
@@ -622,10 +649,13 @@ class RowSet:
         self.dst, self.src = list(dst), list(dst if src is None else src)
         if len(self.dst) != len(self.src):
             raise ValueError("RowSet: as many src as dst tensors are required")
-        for d, s in zip(self.dst, self.src):
-            _dense("dst", d, d.shape, d.dtype)
-            _dense("src", s, (s.shape[0],) + tuple(d.shape[1:]), d.dtype)
         n = len(self.dst)
+        self.device = self.dst[0].get_device() if n else None
+        if n and self.device != torch.cuda.current_device():
+            raise ValueError("RowSet: libfastmamba takes CUDA tensors on the current device")
+        for d, s in zip(self.dst, self.src):
+            _dense("dst", d, d.shape, (d.dtype,), self.device)
+            _dense("src", s, s.shape[:1] + d.shape[1:], (d.dtype,), self.device)
         if n and len({(d.shape[0], s.shape[0]) for d, s in zip(self.dst, self.src)}) != 1:
             raise ValueError("RowSet: every buffer must have the same number of rows")
         self.dst_rows, self.src_rows = (self.dst[0].shape[0], self.src[0].shape[0]) if n else (0, 0)
@@ -638,10 +668,12 @@ class RowSet:
 def reorder_rows(rows: RowSet, parent, src_beams=None, stream=None):
     """dst[b, j] = src[b, parent[b, j]] for every buffer of the set; parent
     [B, beams] int32.  src_beams: beams per batch entry of src (default: as dst)."""
+    dev, st = _place(stream)
     B, beams = parent.shape
     sb = beams if src_beams is None else src_beams
-    if rows.dst and (rows.dst_rows != B * beams or rows.src_rows != B * sb):
-        raise ValueError(f"reorder_rows: {rows.dst_rows} and {rows.src_rows} rows, expected "
-                         f"{B * beams} and {B * sb}")
-    _check(load().fm_reorder_rows(rows._src, rows._dst, rows._row_bytes, len(rows.dst), B, sb, beams,
-                                  _dense("parent", parent, (B, beams), torch.int32), _s(stream)))
+    n = len(rows.dst)
+    if n and (rows.dst_rows != B * beams or rows.src_rows != B * sb or rows.device != dev):
+        raise ValueError(f"reorder_rows: {rows.dst_rows} and {rows.src_rows} rows on device "
+                         f"{rows.device}, expected {B * beams} and {B * sb} on {dev}")
+    _check(load().fm_reorder_rows(rows._src, rows._dst, rows._row_bytes, n, B, sb, beams,
+                                  _dense("parent", parent, (B, beams), _T_I32, dev), st))

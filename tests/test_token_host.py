@@ -120,18 +120,43 @@ def test_reorder_refusals(so):
     assert ro(n=0, src=None) == OK and ro(B=0) == OK
 
 
-def test_python_checks():
-    """The binding refuses what the library could not see: types, shapes, devices."""
+def test_python_checks(monkeypatch):
+    """The binding refuses what the library could not see: types, shapes, strides
+    and devices."""
     from quantized_state_space_mamba2_b200 import lib
-    z = torch.zeros
+    monkeypatch.setattr(lib, "_place", lambda stream: (-1, 0))  # host tensors stand for the device's
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    z, i8, i32, f8 = torch.zeros, torch.int8, torch.int32, torch.float8_e4m3fn
+    refused = [
+        ("dtype", lambda: lib.add_norm_quant(z(2, 32, dtype=torch.float16), z(32), z(2, 32, dtype=i8), z(2))),
+        ("shape", lambda: lib.add_norm_quant(z(2, 32), z(31), z(2, 32, dtype=i8), z(2))),
+        ("shape", lambda: lib.add_norm_quant(z(2, 32), z(32), z(2, 32, dtype=i8), z(2, 1))),
+        ("shape", lambda: lib.add_norm_quant(z(2, 32), z(32), z(2, 32).to(f8), z(2))),
+        ("column stride", lambda: lib.add_norm_quant(z(32, 2).t(), z(32), z(2, 32, dtype=i8), z(2))),
+        ("shape", lambda: lib.fp8_gemm(z(2, 32).to(f8), z(2, 1), z(3, 16).to(f8), z(1, 1), z(2, 3))),
+        ("shape", lambda: lib.fp8_gemm(z(2, 32).to(f8), z(2, 1), z(3, 32).to(f8), z(1, 1), z(2, 4))),
+        ("dtype", lambda: lib.fp8_gemm(z(2, 32), z(2, 1), z(3, 32).to(f8), z(1, 1), z(2, 3))),
+        ("scales", lambda: lib.embed_rows(z(2, dtype=i32), z(4, 16), z(2, 16), table_s=z(1, 1))),
+        ("scales", lambda: lib.embed_rows(z(2, dtype=i32), z(4, 16).to(f8), z(2, 16))),
+        ("dtype", lambda: lib.embed_rows(z(2, dtype=torch.int64), z(4, 16), z(2, 16))),
+        ("one stride", lambda: lib.beam_select(z(2, 5, 9)[:, :3], z(2, 3), z(2, 3), z(2, 3, dtype=i32),
+                                               z(2, 3, dtype=i32), z(999))),
+        ("dtype", lambda: lib.beam_select(z(2, 3, 9), z(2, 3), z(2, 3), z(2, 3, dtype=torch.int64),
+                                          z(2, 3, dtype=i32), z(999))),
+        ("rows", lambda: lib.reorder_rows(lib.RowSet([z(8, 4)]), z(2, 3, dtype=i32))),
+        ("number of rows", lambda: lib.RowSet([z(8, 4), z(6, 4)])),
+        ("shape", lambda: lib.RowSet([z(8, 4)], [z(2, 5)])),
+    ]
+    for i, (why, call) in enumerate(refused):
+        with pytest.raises(ValueError, match=why):
+            call()
+            pytest.fail(f"refusal {i} ({why}) did not come")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(lib, "_place", lambda stream: (0, 0))
     with pytest.raises(ValueError, match="CUDA"):
-        lib.add_norm_quant(z(2, 32), z(32), z(2, 32, dtype=torch.int8), z(2))
-    with pytest.raises(ValueError, match="dtype"):
-        lib.add_norm_quant(z(2, 32, dtype=torch.float16), z(32), z(2, 32, dtype=torch.int8), z(2))
-    with pytest.raises(ValueError, match="shape"):
-        lib.fp8_gemm(z(2, 32), z(2, 1), z(3, 32), z(1, 1), z(2, 4))
-    with pytest.raises(ValueError, match="scales"):
-        lib.embed_rows(z(2, dtype=torch.int32), z(4, 16), z(2, 16), table_s=z(1, 1))
+        lib.add_norm_quant(z(2, 32), z(32), z(2, 32, dtype=i8), z(2))
+    with pytest.raises(ValueError, match="CUDA"):
+        lib.RowSet([z(8, 4)])
 
 
 # ------------------------------------------------------------------ the plain forms
