@@ -131,8 +131,8 @@ static fm_status launch_fp8(const void *A, const void *W, long long K, const Fp8
                             cudaStream_t st) {
   if (a.M <= 16) return launch_fp8_small<16, 11, TY>(A, W, K, a, st);
   if (a.M <= 32) return launch_fp8_small<32, 10, TY>(A, W, K, a, st);
-  if (a.M <= 64) return launch_fp8_small<64, 9, TY>(A, W, K, a, st);
-  if (a.M <= 128) return launch_fp8_small<128, 6, TY>(A, W, K, a, st);
+  if (a.M <= 64) return launch_fp8_small<64, 8, TY>(A, W, K, a, st);
+  if (a.M <= 128) return launch_fp8_small<128, 5, TY>(A, W, K, a, st);
   // 256 columns per tile halve the traffic of A; narrower tiles where those
   // would leave SMs idle
   if ((a.M + kGemmBM - 1) / kGemmBM * ((a.N + 255) / 256) >= sm_count())

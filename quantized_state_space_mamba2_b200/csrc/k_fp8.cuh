@@ -73,8 +73,82 @@ __device__ __forceinline__ void ffma2(unsigned long long &acc, uint32_t lo, uint
       : "+l"(acc)
       : "r"(lo), "r"(hi), "l"(c));
 }
+// (lo, hi) * c
+__device__ __forceinline__ unsigned long long fmul2(float lo, float hi, unsigned long long c) {
+  unsigned long long d;
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tmul.rn.f32x2 %0, v, %3;\n\t}"
+      : "=l"(d)
+      : "f"(lo), "f"(hi), "l"(c));
+  return d;
+}
 __device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
   return ((unsigned long long)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+
+// Bounded wait for the hand-overs of a pipeline, whose limit lies in shared
+// memory (a load of it from global memory costs more than such a wait).  The
+// thread may stay suspended in a poll: polls that return at once take issue
+// slots and shared-memory cycles from the warps at work.
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u /* ns */)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_in(uint64_t *bar, uint32_t parity,
+                                             const unsigned long long &limit) {
+  if (mbar_try_wait(bar, parity)) return true;  // 14 cycles; a poll that may suspend takes 50
+  const unsigned long long t0 = globaltimer();
+  while (true) {
+    if (mbar_poll(bar, parity)) return true;
+    if (globaltimer() - t0 > limit) {
+      raise_error(kErrTimeout);
+      return false;
+    }
+  }
+}
+
+// True in one lane of a converged warp.  The compiler knows that one lane runs
+// the code behind it, and issues tcgen05 and TMA instructions there at once;
+// behind `lane == 0` each of them costs 44 cycles, a commit among them too
+// (measured: 4 MMAs of N = 16 and 2 commits 265 cycles, 157 behind this).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// A position in a ring of N slots and the parity of its current round.  (A
+// counter taken modulo N costs a dependent chain of multiplications per block.)
+template <int N>
+struct RingPos {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      round ^= 1u;
+    }
+  }
+};
+
+// Waits for every copy issued into the ring up to (not including) position
+// `end`: they must have landed before the CTA may exit.  On the normal path all
+// have been consumed and this returns at once.
+template <int N>
+__device__ __forceinline__ void ring_drain(uint64_t *full_bar, const RingPos<N> &end) {
+  for (uint32_t i = 0; i < N; ++i) {
+    // slot i was last filled in this round (i < end.at) or the one before,
+    // whose parity is also what an unused slot's preceding phase counts as
+    const uint32_t round = i < end.at ? end.round : end.round ^ 1u;
+    if (!mbar_drain(&full_bar[i], round)) break;
+  }
 }
 
 struct Fp8Args {
@@ -163,7 +237,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int num_tiles = a.m_tiles * a.n_tiles;
 
+  __shared__ unsigned long long limit;  // of the waits, ns
   if (threadIdx.x == 0) {
+    limit = *(volatile unsigned long long *)&g_wait_limit_ns;
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full_bar[i], 1);
       mbar_init(&empty_bar[i], 1);
@@ -197,51 +273,54 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFp8RegsLoad));
+    // every lane of the two warps runs the loops and the waits, one issues
+    const bool lead = elect_one();
     if (warp == 0) {
-      if (lane == 0) {
-        bool ok = !(g_test_stall & kStallGemm);
-        long long it = 0;
-        for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-          const int m0 = (t / a.n_tiles) * kGemmBM, n0 = (t % a.n_tiles) * BN;
-          for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-            const int s = (int)(it % STAGES);
-            if (!mbar_wait(&empty_bar[s], ((uint32_t)(it / STAGES) & 1u) ^ 1u)) {
-              ok = false;
-              break;
-            }
+      bool ok = !(g_test_stall & kStallGemm);
+      RingPos<STAGES> ring;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        const int m0 = (t / a.n_tiles) * kGemmBM, n0 = (t % a.n_tiles) * BN;
+        for (int kb = 0; kb < a.nkb; ++kb, ring.next()) {
+          const uint32_t s = ring.at;
+          if (!mbar_wait_in(&empty_bar[s], ring.round ^ 1u, limit)) {
+            ok = false;
+            break;
+          }
+          if (lead) {
             mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(Sm::kA + Sm::kB));
             tma_load_2d(sA + s * Sm::kA, &tmA, kb * kGemmBK, m0, &full_bar[s]);
             tma_load_2d(sB + s * Sm::kB, &tmB, kb * kGemmBK, n0, &full_bar[s]);
           }
         }
-        // every copy issued must have landed before the CTA may exit
-        for (long long j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-          if (!mbar_drain(&full_bar[j % STAGES], (uint32_t)(j / STAGES) & 1u)) break;
       }
+      // every copy issued must have landed before the CTA may exit
+      if (lead) ring_drain<STAGES>(full_bar, ring);
     } else if (warp == 1) {
-      if (lane == 0) {
-        constexpr uint32_t idesc = e4m3_idesc(kGemmBM, BN);
-        long long it = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x)
-          for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-            const int s = (int)(it % STAGES), acc = (int)(it % kAcc);
-            if (!mbar_wait(&tempty[acc], ((uint32_t)(it / kAcc) & 1u) ^ 1u) ||
-                !mbar_wait(&full_bar[s], (uint32_t)(it / STAGES) & 1u)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t ad = sw128_desc(smem_u32(sA + s * Sm::kA));
-            const uint64_t bd = sw128_desc(smem_u32(sB + s * Sm::kB));
+      constexpr uint32_t idesc = e4m3_idesc(kGemmBM, BN);
+      const uint64_t ad0 = sw128_desc(smem_u32(sA)), bd0 = sw128_desc(smem_u32(sB));
+      RingPos<STAGES> ring;
+      RingPos<kAcc> out;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x)
+        for (int kb = 0; kb < a.nkb; ++kb, ring.next(), out.next()) {
+          const uint32_t s = ring.at, acc = out.at;
+          if (!mbar_wait_in(&tempty[acc], out.round ^ 1u, limit) ||
+              !mbar_wait_in(&full_bar[s], ring.round, limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lead) {
+            const uint64_t ad = ad0 + s * (Sm::kA / 16), bd = bd0 + s * (Sm::kB / 16);
 #pragma unroll
             for (int k = 0; k < kGemmBK / 32; ++k)
-              mma_e4m3(tmem_base + (uint32_t)(acc * BN), ad + (uint64_t)(2 * k),
-                       bd + (uint64_t)(2 * k), idesc, k > 0 ? 1u : 0u);
+              mma_e4m3(tmem_base + acc * BN, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), idesc,
+                       k > 0 ? 1u : 0u);
             mma_commit(&empty_bar[s]);
             mma_commit(&tfull[acc]);
           }
-        // wait for every MMA issued so far before TMEM can be released
+        }
+      if (lead) {  // wait for every MMA issued so far before TMEM can be released
         mma_commit(drain_bar);
         mbar_drain(drain_bar, 0);
       }
@@ -250,7 +329,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFp8RegsAcc));
     const int e = warp - 4, quarter = warp & 3, half = e / 4;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kCols);
-    long long it = 0;
+    RingPos<kAcc> in;
     bool ok = true;
     for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
       const long long m0 = (long long)(t / a.n_tiles) * kGemmBM + quarter * 32;
@@ -262,15 +341,19 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
       unsigned long long acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = 0ull;
-      float ca = pa[0], cw = pw[0];
-      for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-        const int buf = (int)(it % kAcc);
-        const float c = __fmul_rn(ca, cw);
-        if (kb + 1 < a.nkb) {  // the next block's scales, a block ahead
-          ca = pa[kb + 1];
-          cw = pw[kb + 1];
-        }
-        ok = mbar_wait(&tfull[buf], (uint32_t)(it / kAcc) & 1u);
+      // the scales are fetched well ahead (they come from L2: shared memory
+      // leaves L1 next to nothing): a row's own two blocks ahead, the column
+      // block's, which the warp shares, 32 blocks in the lanes at a time
+      float ca = pa[0], ca1 = pa[min(1, a.nkb - 1)];
+      float cw = pw[min(lane, a.nkb - 1)];
+#pragma unroll 1
+      for (int kb = 0; kb < a.nkb; ++kb, in.next()) {
+        const uint32_t buf = in.at;
+        if (kb && (kb & 31) == 0) cw = pw[min(kb + lane, a.nkb - 1)];
+        const float c = __fmul_rn(ca, __shfl_sync(0xffffffffu, cw, kb & 31));
+        ca = ca1;
+        if (kb + 2 < a.nkb) ca1 = pa[kb + 2];
+        ok = mbar_wait_in(&tfull[buf], in.round, limit);
         ok = __all_sync(0xffffffffu, ok);  // tcgen05.ld is warp-collective
         if (!ok) break;
         tc_fence_after();
@@ -335,15 +418,18 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 // A decode batch: the weights' rows take the MMA's M side (128 per tile) and
 // the MP >= M activation rows its N side, so a tile costs what its real rows
 // cost and the weights stream past once.  Lane = weight row n, column =
-// activation row m; s_a s_w of the block is staged in shared memory, one
-// number per column.  The accumulators and the warps are as above (four
-// warps; eight for MP = 128, each with 64 columns).
+// activation row m: s_w is one number per tile and block, and s_a, which is
+// the same for every tile, waits in shared memory (block by block, the MP rows
+// of a block side by side; kChunk blocks at a time).  The columns are split
+// over as many warps as leaves each 16 (MP = 128: 32): a block's read-back is a
+// chain of waits, which the four warps of a scheduler take in turns.
 template <int MP, int STAGES>
 struct Fp8SmallSmem {
   static constexpr int kW = kGemmBM * kGemmBK, kA = MP * kGemmBK;
-  static constexpr int kEpi = MP > 64 ? 8 : 4;
+  static constexpr int kEpi = MP > 64 ? 16 : MP / 4;  // 16 columns each, 32 of MP = 128
   static constexpr int kAcc = 512 / MP < 4 ? 512 / MP : 4;
-  static constexpr int kBytes = 1024 + STAGES * (kW + kA) + 2 * MP * 4 +
+  static constexpr int kChunk = 64;
+  static constexpr int kBytes = 1024 + STAGES * (kW + kA) + kChunk * MP * 4 +
                                 (2 * STAGES + 2 * kAcc + 1) * 8 + 16;
 };
 
@@ -354,15 +440,14 @@ __global__ void __launch_bounds__(64 + 32 * Fp8SmallSmem<MP, STAGES>::kEpi, 1)
   using Sm = Fp8SmallSmem<MP, STAGES>;
   constexpr int kAcc = Sm::kAcc, kEpi = Sm::kEpi;
   constexpr int kCols = MP / (kEpi / 4);  // columns per epilogue warp
-  constexpr int kLd = kCols < 32 ? kCols : 32;
   constexpr uint32_t kTmem = kAcc * MP;  // a power of two >= 64
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *sW = smem;
   uint8_t *sA = smem + STAGES * Sm::kW;
-  float *coef = reinterpret_cast<float *>(sA + STAGES * Sm::kA);  // [2][MP]
-  uint64_t *full_bar = reinterpret_cast<uint64_t *>(coef + 2 * MP);
+  float *coef = reinterpret_cast<float *>(sA + STAGES * Sm::kA);  // [kChunk][MP]
+  uint64_t *full_bar = reinterpret_cast<uint64_t *>(coef + Sm::kChunk * MP);
   uint64_t *empty_bar = full_bar + STAGES;
   uint64_t *tfull = empty_bar + STAGES;
   uint64_t *tempty = tfull + kAcc;
@@ -370,7 +455,9 @@ __global__ void __launch_bounds__(64 + 32 * Fp8SmallSmem<MP, STAGES>::kEpi, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain_bar + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  __shared__ unsigned long long limit;  // of the waits, ns
   if (threadIdx.x == 0) {
+    limit = *(volatile unsigned long long *)&g_wait_limit_ns;
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full_bar[i], 1);
       mbar_init(&empty_bar[i], 1);
@@ -398,106 +485,120 @@ __global__ void __launch_bounds__(64 + 32 * Fp8SmallSmem<MP, STAGES>::kEpi, 1)
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 2) {
+    const bool lead = elect_one();
+    RingPos<STAGES> ring;
+    if (warp == 0) {
       bool ok = !(g_test_stall & kStallGemm);
-      long long it = 0;
       for (int t = blockIdx.x; t < a.n_tiles && ok; t += gridDim.x)
-        for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-          const int s = (int)(it % STAGES);
-          if (!mbar_wait(&empty_bar[s], ((uint32_t)(it / STAGES) & 1u) ^ 1u)) {
+        for (int kb = 0; kb < a.nkb; ++kb, ring.next()) {
+          const uint32_t s = ring.at;
+          if (!mbar_wait_in(&empty_bar[s], ring.round ^ 1u, limit)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(Sm::kW + Sm::kA));
-          tma_load_2d(sW + s * Sm::kW, &tmW, kb * kGemmBK, t * kGemmBM, &full_bar[s]);
-          tma_load_2d(sA + s * Sm::kA, &tmA, kb * kGemmBK, 0, &full_bar[s]);
+          if (lead) {
+            mbar_arrive_expect_tx(&full_bar[s], (uint32_t)(Sm::kW + Sm::kA));
+            tma_load_2d(sW + s * Sm::kW, &tmW, kb * kGemmBK, t * kGemmBM, &full_bar[s]);
+            tma_load_2d(sA + s * Sm::kA, &tmA, kb * kGemmBK, 0, &full_bar[s]);
+          }
         }
-      for (long long j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-        if (!mbar_drain(&full_bar[j % STAGES], (uint32_t)(j / STAGES) & 1u)) break;
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+      if (lead) ring_drain<STAGES>(full_bar, ring);
+    } else {
       constexpr uint32_t idesc = e4m3_idesc(kGemmBM, MP);
-      long long it = 0;
+      const uint64_t wd0 = sw128_desc(smem_u32(sW)), ad0 = sw128_desc(smem_u32(sA));
+      RingPos<kAcc> out;
       bool ok = true;
       for (int t = blockIdx.x; t < a.n_tiles && ok; t += gridDim.x)
-        for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-          const int s = (int)(it % STAGES), acc = (int)(it % kAcc);
-          if (!mbar_wait(&tempty[acc], ((uint32_t)(it / kAcc) & 1u) ^ 1u) ||
-              !mbar_wait(&full_bar[s], (uint32_t)(it / STAGES) & 1u)) {
+        for (int kb = 0; kb < a.nkb; ++kb, ring.next(), out.next()) {
+          const uint32_t s = ring.at, acc = out.at;
+          if (!mbar_wait_in(&tempty[acc], out.round ^ 1u, limit) ||
+              !mbar_wait_in(&full_bar[s], ring.round, limit)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t wd = sw128_desc(smem_u32(sW + s * Sm::kW));
-          const uint64_t ad = sw128_desc(smem_u32(sA + s * Sm::kA));
+          if (lead) {
+            const uint64_t wd = wd0 + s * (Sm::kW / 16), ad = ad0 + s * (Sm::kA / 16);
 #pragma unroll
-          for (int k = 0; k < kGemmBK / 32; ++k)
-            mma_e4m3(tmem_base + (uint32_t)(acc * MP), wd + (uint64_t)(2 * k),
-                     ad + (uint64_t)(2 * k), idesc, k > 0 ? 1u : 0u);
-          mma_commit(&empty_bar[s]);
-          mma_commit(&tfull[acc]);
+            for (int k = 0; k < kGemmBK / 32; ++k)
+              mma_e4m3(tmem_base + acc * MP, wd + (uint64_t)(2 * k), ad + (uint64_t)(2 * k), idesc,
+                       k > 0 ? 1u : 0u);
+            mma_commit(&empty_bar[s]);
+            mma_commit(&tfull[acc]);
+          }
         }
-      mma_commit(drain_bar);
-      mbar_drain(drain_bar, 0);
+      if (lead) {
+        mma_commit(drain_bar);
+        mbar_drain(drain_bar, 0);
+      }
     }
   } else {
     const int quarter = warp & 3, part = (warp - 2) / 4, et = threadIdx.x - 64;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * kCols);
-    const float *pa = a.s_a + min((long long)et, a.M - 1) * a.nkb;  // thread et < MP: column et
-    long long it = 0;
+    // the next kChunk blocks' s_a (zeros for columns past M)
+    auto stage = [&](int kb0) {
+      asm volatile("bar.sync 1, %0;" ::"r"(32 * kEpi) : "memory");
+      const int nb = min(Sm::kChunk, a.nkb - kb0);
+      for (int i = et; i < nb * MP; i += 32 * kEpi) {
+        const int m = i / nb, kb = i - m * nb;
+        coef[kb * MP + m] = m < a.M ? a.s_a[(long long)m * a.nkb + kb0 + kb] : 0.0f;
+      }
+      asm volatile("bar.sync 1, %0;" ::"r"(32 * kEpi) : "memory");
+    };
+    const bool resident = a.nkb <= Sm::kChunk;
+    if (resident) stage(0);
+    RingPos<kAcc> in;
     bool ok = true;
-    // after a failed wait a warp skips its work but still meets the others at
-    // every block's barrier
+    // after a failed wait a warp skips its work but still meets the others
+    // wherever scales are staged
     for (int t = blockIdx.x; t < a.n_tiles; t += gridDim.x) {
       const float *pw = a.s_w + (long long)t * a.nkb;
       unsigned long long acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = 0ull;
-      float ca = et < MP ? pa[0] : 0.0f, cw = pw[0];
-      for (int kb = 0; kb < a.nkb; ++kb, ++it) {
-        const int buf = (int)(it % kAcc);
-        // this block's factors; the buffer was last read two blocks ago, before
-        // every warp passed the previous block's barrier
-        float *cf = coef + (it & 1) * MP;
-        if (et < MP) cf[et] = __fmul_rn(ca, cw);
-        if (kb + 1 < a.nkb) {
-          if (et < MP) ca = pa[kb + 1];
-          cw = pw[kb + 1];
-        }
-        asm volatile("bar.sync 1, %0;" ::"r"(32 * kEpi) : "memory");
-        if (ok) ok = mbar_wait(&tfull[buf], (uint32_t)(it / kAcc) & 1u);
+      float cw = pw[0];
+#pragma unroll 1
+      for (int kb = 0; kb < a.nkb; ++kb, in.next()) {
+        if (!resident && kb % Sm::kChunk == 0) stage(kb);
+        const uint32_t buf = in.at;
+        const float4 *cf = reinterpret_cast<const float4 *>(coef + kb % Sm::kChunk * MP + part * kCols);
+        const unsigned long long w2 = pack2(cw, cw);
+        if (kb + 1 < a.nkb) cw = pw[kb + 1];
+        unsigned long long c[8];  // 16 columns' factors
+        auto factors = [&](int q) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 v = cf[4 * q + j];
+            c[2 * j] = fmul2(v.x, v.y, w2);
+            c[2 * j + 1] = fmul2(v.z, v.w, w2);
+          }
+        };
+        factors(0);  // while the block is multiplied
+        if (ok) ok = mbar_wait_in(&tfull[buf], in.round, limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         tc_fence_after();
-        const unsigned long long *cf2 =
-            reinterpret_cast<const unsigned long long *>(cf + part * kCols);
 #pragma unroll
-        for (int q = 0; q < kCols / kLd; ++q) {
-          uint32_t r[32];
-          if constexpr (kLd == 32) {
-            tmem_ld32_issue(lane_base + (uint32_t)(buf * MP + 32 * q), r);
-            tmem_ld_wait(r);
-          } else {
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-                "tcgen05.wait::ld.sync.aligned;"
-                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                  "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                  "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                : "r"(lane_base + (uint32_t)(buf * MP))
-                : "memory");
-          }
-          if (q + 1 == kCols / kLd) {
+        for (int q = 0; q < kCols / 16; ++q) {
+          uint32_t r[16];
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+              "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+              "tcgen05.wait::ld.sync.aligned;"
+              : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+                "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+              : "r"(lane_base + buf * MP + 16 * q)
+              : "memory");
+          if (q + 1 == kCols / 16) {  // the last load has completed: hand the buffer back
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[buf]);
           }
 #pragma unroll
-          for (int j = 0; j < kLd / 2; ++j)
-            ffma2(acc[kLd / 2 * q + j], r[2 * j], r[2 * j + 1], cf2[kLd / 2 * q + j]);
+          for (int j = 0; j < 8; ++j) ffma2(acc[8 * q + j], r[2 * j], r[2 * j + 1], c[j]);
+          if (q + 1 < kCols / 16) factors(q + 1);
         }
       }
       const long long n = (long long)t * kGemmBM + quarter * 32 + lane;

@@ -206,6 +206,17 @@ def test_product_is_the_same_every_time_and_rows_are_independent(lib):
     assert bool(again[5].isnan().all()) and bool(again[3].isfinite().all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K,ldy", [(2500, 2700, 400, 2700), (4001, 1301, 144, 1301), (300, 9601, 16, 9601),
+                                       (8200, 700, 2560, 704), (257, 19000, 640, 19013),
+                                       (20000, 130, 128, 136)])
+def test_product_on_pairs_of_ctas(lib, M, N, K, ldy, dtype):
+    g = gen(M + N)
+    buf = torch.full((M, ldy), 3.0, device="cuda", dtype=dtype)
+    check_product(lib, *product_case(g, M, N, K, 0.3), buf[:, :N])
+    assert bool((buf[:, N:] == 3.0).all())
+
+
 def test_product_large(lib):
     # more tiles than SMs in both directions, and K of 20 blocks
     g = gen(12)
