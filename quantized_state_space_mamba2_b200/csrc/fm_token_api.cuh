@@ -169,18 +169,29 @@ extern "C" fm_status fm_fp8_gemm(const void *A, const float *s_a, int64_t M, con
 }
 
 // ------------------------------------------------------------------ beam selection
-static size_t beam_ws_keys(int64_t rows, int n_out) {
-  return ((size_t)rows * n_out * 8 + 255) / 256 * 256;
+// Logits per thread of a chunk: 32 where that gives two CTAs per SM (of 148),
+// fewer for the latency of small selections.
+static int beam_elems(int64_t rows, int64_t V) {
+  const auto ctas = [&](int e) { return rows * ((V + kBeamThreads * e - 1) / (kBeamThreads * e)); };
+  return ctas(32) >= 296 ? 32 : ctas(16) >= 296 ? 16 : 8;
 }
+static int64_t beam_chunks(int64_t rows, int64_t V) {
+  const int64_t n = kBeamThreads * beam_elems(rows, V);
+  return (V + n - 1) / n;
+}
+static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
 static bool beam_sizes_ok(int B, int beams, int64_t V, int n_out) {
   return B >= 0 && beams >= 1 && beams <= kBeamMax && n_out >= 1 && n_out <= kBeamMax && V >= 1 &&
-         V <= 0x7FFFFFFF && (int64_t)B * beams <= 0x7FFFFFFF;
+         V <= 0x7FFFFFFF && (int64_t)B * beams <= 0x7FFFFFFF &&
+         (int64_t)B * beams * beam_chunks((int64_t)B * beams, V) <= 0x7FFFFFFF;
 }
 
 extern "C" size_t fm_beam_workspace_bytes(int B, int beams, int64_t V, int n_out) {
   if (!beam_sizes_ok(B, beams, V, n_out)) return 0;
   const int64_t rows = (int64_t)B * beams;
-  return beam_ws_keys(rows, n_out) + (size_t)rows * 8;
+  const size_t chunks = (size_t)rows * beam_chunks(rows, V);
+  return round256(chunks * n_out * 8) + round256(chunks * 8) + round256(chunks * 4);
 }
 
 extern "C" fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t ld, int B, int beams,
@@ -213,19 +224,24 @@ extern "C" fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t l
     return fail(FM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", __func__, need);
   NEED(ws);
   const int64_t rows = (int64_t)B * beams;
+  const int S = (int)beam_chunks(rows, V), E = beam_elems(rows, V);
+  const size_t chunks = (size_t)rows * S;
   unsigned long long *keys = (unsigned long long *)ws;
-  double *lse = (double *)((char *)ws + beam_ws_keys(rows, n_out));
+  double *sums = (double *)((char *)ws + round256(chunks * n_out * 8));
+  float *tops = (float *)((char *)sums + round256(chunks * 8));
   cudaStream_t st = (cudaStream_t)stream;
-  if (type == FM_F32)
-    FM_TRY(launch_ex("k_beam_rows", k_beam_rows<float>, (unsigned)rows, kBeamThreads, 0, st,
-                     (const float *)logits, (long long)ld, (unsigned)V, n_out, keys, lse));
-  else
-    FM_TRY(launch_ex("k_beam_rows", k_beam_rows<__nv_bfloat16>, (unsigned)rows, kBeamThreads, 0, st,
-                     (const __nv_bfloat16 *)logits, (long long)ld, (unsigned)V, n_out, keys, lse));
-  FM_TRY(launched("k_beam_rows"));
-  FM_TRY(launch_ex("k_beam_merge", k_beam_merge, (unsigned)B, 32, 0, st,
-                   (const unsigned long long *)keys, (const double *)lse, beams, scores, finished,
-                   eos, n_out, out_scores, parent, token, out_finished));
+  auto go = [&](auto t) -> fm_status {
+    using T = decltype(t);
+    auto kern = E == 32 ? k_beam_chunks<T, 32> : E == 16 ? k_beam_chunks<T, 16> : k_beam_chunks<T, 8>;
+    return launch_ex("k_beam_chunks", kern, (unsigned)chunks, kBeamThreads, 0, st,
+                     (const T *)logits, (long long)ld, (unsigned)V, S, n_out, scores, finished, keys,
+                     tops, sums);
+  };
+  FM_TRY(type == FM_F32 ? go(float()) : go(__nv_bfloat16()));
+  FM_TRY(launched("k_beam_chunks"));
+  FM_TRY(launch_ex("k_beam_merge", k_beam_merge, (unsigned)B, 32 * beams, 0, st,
+                   (const unsigned long long *)keys, (const float *)tops, (const double *)sums, S,
+                   beams, scores, finished, eos, n_out, out_scores, parent, token, out_finished));
   return launched("k_beam_merge");
 }
 

@@ -4,8 +4,16 @@
 //   c[k, v] = score[k] + l[k, v] - lse[k],
 // and the n best of a batch entry are taken, ties to the lowest k V + v.
 // Within a beam the order of c is that of l, so each beam's n largest logits
-// are enough: k_beam_rows finds them and lse, k_beam_merge the n best of the
-// beams' lists, by c in 64 bits.
+// are enough.  k_beam_chunks reads the logits once: a CTA holds a chunk of one
+// beam's row in registers and leaves its maximum, its sum of exponentials and
+// its n largest logits; k_beam_merge joins the chunks' sums and lists and takes
+// the n best of the beams' lists, by c in 64 bits.
+//
+// The reading is bound by memory.  The n largest of a chunk are found without
+// sorting it: the n-th largest of 32 group maxima (groups of 8 threads) is not
+// above the chunk's n-th largest value, so few values reach it; they are
+// collected and ranked against each other.  Where ties or masks let more than
+// kBeamCap through, n rounds of a maximum over the registers find them instead.
 #pragma once
 #include <cuda_bf16.h>
 #include "fm_common.cuh"
@@ -35,10 +43,65 @@ __device__ __forceinline__ unsigned beam_key_index(unsigned long long k) {
 __device__ __forceinline__ float beam_logit(float l) {
   return fminf(fmaxf(l, -INFINITY), 3.402823466e38f) + 0.0f;
 }
-__device__ __forceinline__ float beam_load(const float *p) { return beam_logit(*p); }
-__device__ __forceinline__ float beam_load(const __nv_bfloat16 *p) {
-  return beam_logit(__bfloat162float(*p));
-}
+constexpr int kBeamCap = 512;
+
+// A thread's E elements of a row's chunk: groups of 16 bytes, 256 threads side
+// by side.  Which thread holds an element does not depend on where the row lies
+// in memory, so equal rows have equal sums and their ties stay ties.  In a row
+// that is not 16-byte aligned a group is cut from the two aligned vectors that
+// cover it (the second is the neighbour's first, in L1).  Elements behind the
+// row are -inf.
+template <typename T, int E>
+struct BeamChunk {
+  static constexpr int kVec = 16 / (int)sizeof(T);  // elements per group
+  float v[E];
+  unsigned first;
+  __device__ __forceinline__ unsigned at(int i) const {  // the element's index
+    return first + (unsigned)(i / kVec * (kBeamThreads * kVec) + i % kVec);
+  }
+  __device__ __forceinline__ void load(const T *row, unsigned V, unsigned chunk) {
+    const unsigned skew = (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u);  // bytes
+    first = chunk * (unsigned)(kBeamThreads * E) + threadIdx.x * kVec;
+#pragma unroll
+    for (int j = 0; j < E / kVec; ++j) {
+      const unsigned long long p = (unsigned long long)first + j * (kBeamThreads * kVec);
+      if (p + 2 * kVec <= V) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + p) - skew);
+        const uint4 x = q[0];
+        uint32_t w[8] = {x.x, x.y, x.z, x.w, 0, 0, 0, 0};
+        if (skew) {  // the same for the whole CTA
+          const uint4 y = q[1];
+          w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+          if (skew & 8) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+          }
+          if (skew & 4) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+          }
+          if (sizeof(T) == 2 && (skew & 2)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 4) {
+            v[4 * j + i] = beam_logit(__uint_as_float(w[i]));
+          } else {
+            v[8 * j + 2 * i] = beam_logit(__uint_as_float(w[i] << 16));
+            v[8 * j + 2 * i + 1] = beam_logit(__uint_as_float(w[i] & 0xFFFF0000u));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          v[kVec * j + i] = p + i < V ? beam_logit((float)row[p + i]) : -INFINITY;
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ unsigned long long cta_max_key(unsigned long long k,
                                                           unsigned long long *s_red) {
@@ -55,72 +118,179 @@ __device__ __forceinline__ unsigned long long cta_max_key(unsigned long long k,
   return k;
 }
 
-// Workspace: keys [rows, n_out] (descending, 0 where there is none), lse [rows].
-template <typename T>
+// One CTA per chunk of 256 E logits, S chunks per row.
+// Workspace: keys [rows, S, n_out] (descending, 0 where there is none), top
+// [rows, S] (the chunk's maximum) and sum [rows, S] (of exp(l - top)).
+// A row that cannot win by its logits -- its beam finished or dead -- is not read.
+template <typename T, int E>
 __global__ void __launch_bounds__(kBeamThreads)
-    k_beam_rows(const T *__restrict__ logits, long long ld, unsigned V, int n_out,
-                unsigned long long *__restrict__ keys, double *__restrict__ lse) {
+    k_beam_chunks(const T *__restrict__ logits, long long ld, unsigned V, int S, int n_out,
+                  const float *__restrict__ scores, const uint8_t *__restrict__ finished,
+                  unsigned long long *__restrict__ keys, float *__restrict__ tops,
+                  double *__restrict__ sums) {
   pdl_wait();
   pdl_trigger();
-  __shared__ unsigned long long s_key[kBeamThreads / 32];
+  __shared__ float s_group[32];
   __shared__ double s_sum[kBeamThreads / 32];
-  const T *row = logits + blockIdx.x * ld;
+  __shared__ unsigned long long s_key[kBeamCap];
+  __shared__ int s_count;
+  const unsigned row = blockIdx.x / S, chunk = blockIdx.x - row * S;
+  if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) s_count = 0;
+  BeamChunk<T, E> c;
+  c.load(logits + (long long)row * ld, V, chunk);
+  float m = c.v[0];
+#pragma unroll
+  for (int i = 1; i < E; ++i) m = fmaxf(m, c.v[i]);
+#pragma unroll
+  for (int o = 1; o <= 4; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((lane & 7) == 0) s_group[threadIdx.x >> 3] = m;
+  __syncthreads();
+  // every warp: the chunk's maximum and the n-th largest group maximum
+  const float g = s_group[lane];
+  const float top = warp_max(g);
+  int rank = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float o = __shfl_sync(0xffffffffu, g, j);
+    rank += o > g || (o == g && j < lane);
+  }
+  const float bar = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, rank == n_out - 1)) - 1);
+  float sum = 0.0f;
+  if (top > -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      sum += exp2f((c.v[i] - top) * 1.4426950408889634f);
+      if (c.v[i] >= bar && c.v[i] > -INFINITY) {
+        const int at = atomicAdd(&s_count, 1);
+        if (at < kBeamCap) s_key[at] = beam_key(c.v[i], c.at(i));
+      }
+    }
+  }
+  double total = (double)sum;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) s_sum[warp] = total;
+  __syncthreads();
+  unsigned long long *out = keys + (size_t)blockIdx.x * n_out;
+  const int count = s_count;
+  if (threadIdx.x == 0) {
+    total = s_sum[0];
+    for (int i = 1; i < kBeamThreads / 32; ++i) total += s_sum[i];
+    tops[blockIdx.x] = top;
+    sums[blockIdx.x] = total;
+  }
+  if (count <= kBeamCap) {
+    for (int i = threadIdx.x; i < max(count, n_out); i += kBeamThreads) {
+      if (i >= count) {
+        out[i] = 0;  // fewer values than slots
+        continue;
+      }
+      const unsigned long long k = s_key[i];
+      int r = 0;
+      for (int j = 0; j < count; ++j) r += s_key[j] > k;
+      if (r < n_out) out[r] = k;
+    }
+    return;
+  }
   unsigned long long last = ~0ull;
-  float top = 0.0f;
   for (int n = 0; n < n_out; ++n) {
     unsigned long long best = 0;
-    for (unsigned v = threadIdx.x; v < V; v += kBeamThreads) {
-      const float l = beam_load(row + v);
-      const unsigned long long k = l > -INFINITY ? beam_key(l, v) : 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const unsigned long long k = c.v[i] > -INFINITY ? beam_key(c.v[i], c.at(i)) : 0;
       if (k < last && k > best) best = k;
     }
-    best = cta_max_key(best, s_key);
-    if (n == 0) top = beam_key_logit(best);
-    if (threadIdx.x == 0) keys[(size_t)blockIdx.x * n_out + n] = best;
-    last = best;
-  }
-  double sum = 0.0;
-  for (unsigned v = threadIdx.x; v < V; v += kBeamThreads)
-    sum += (double)expf(beam_load(row + v) - top);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kBeamThreads / 32; ++i) sum += s_sum[i];
-    lse[blockIdx.x] = (double)top + log(sum);
+    last = cta_max_key(best, s_key);
+    if (threadIdx.x == 0) out[n] = last;
   }
 }
 
-// One warp per batch entry: lane k walks beam k's list.
-__global__ void __launch_bounds__(32)
-    k_beam_merge(const unsigned long long *__restrict__ keys, const double *__restrict__ lse,
-                 int beams, const float *scores, const uint8_t *finished, int eos, int n_out,
-                 float *out_scores, int32_t *parent, int32_t *token, uint8_t *out_finished) {
+__device__ __forceinline__ unsigned long long warp_max_key(unsigned long long k) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const unsigned long long x = __shfl_xor_sync(0xffffffffu, k, o);
+    k = x > k ? x : k;
+  }
+  return k;
+}
+
+// One CTA per batch entry, one warp per beam for its log sum and its n largest
+// logits (the largest key below the last one, n times over its chunks' lists),
+// then one warp, lane k at the head of beam k's list.
+__global__ void __launch_bounds__(32 * kBeamMax)
+    k_beam_merge(const unsigned long long *__restrict__ keys, const float *__restrict__ tops,
+                 const double *__restrict__ sums, int S, int beams, const float *scores,
+                 const uint8_t *finished, int eos, int n_out, float *out_scores, int32_t *parent,
+                 int32_t *token, uint8_t *out_finished) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x;
-  const long long row = (long long)blockIdx.x * beams + lane;
-  const bool live = lane < beams;
-  const float sc = live ? scores[row] : -INFINITY;
-  const bool done = live && finished && finished[row];
-  const bool dead = !(sc > -INFINITY);
-  const double base = live && !done ? lse[row] : 0.0;
+  __shared__ unsigned long long s_list[kBeamMax][kBeamMax];
+  __shared__ double s_lse[kBeamMax];
+  __shared__ float s_score[kBeamMax];
+  __shared__ uint8_t s_done[kBeamMax];
+  const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5;
+  const long long row = (long long)blockIdx.x * beams + beam;
+  const float score = scores[row];
+  const bool finish = finished && finished[row], dead = !(score > -INFINITY);
+  if (lane == 0) {
+    s_score[beam] = score;
+    s_done[beam] = finish;
+  }
+  if (!finish && !dead) {
+    const float *tp = tops + row * S;
+    const double *sp = sums + row * S;
+    float m = -INFINITY;
+    for (int i = lane; i < S; i += 32) m = fmaxf(m, tp[i]);
+    m = warp_max(m);
+    double t = 0.0;
+    for (int i = lane; i < S; i += 32)
+      if (sp[i] > 0.0) t += sp[i] * exp((double)tp[i] - (double)m);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) s_lse[beam] = (double)m + log(t);
+    const unsigned long long *kp = keys + row * S * n_out;
+    const int all = S * n_out;
+    constexpr int kHold = 8;  // keys per lane held in registers
+    unsigned long long own[kHold], last = ~0ull;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) own[i] = 32 * i + lane < all ? kp[32 * i + lane] : 0;
+    for (int n = 0; n < n_out; ++n) {
+      unsigned long long best = 0;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+        if (own[i] < last && own[i] > best) best = own[i];
+      for (int i = 32 * kHold + lane; i < all; i += 32)
+        if (kp[i] < last && kp[i] > best) best = kp[i];
+      last = warp_max_key(best);
+      if (lane == 0) s_list[beam][n] = last;
+      if (last == 0) {
+        for (int j = n + 1 + lane; j < n_out; j += 32) s_list[beam][j] = 0;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  if (beam != 0) return;
+  const bool live = lane < beams && s_score[lane < beams ? lane : 0] > -INFINITY;
+  const double sc = live ? (double)s_score[lane] : 0.0;
+  const bool done = live && s_done[lane];
+  const double base = live && !done ? s_lse[lane] : 0.0;
   int at = 0;
   auto value = [&](unsigned &v) -> double {
-    if (dead || !live) return -INFINITY;
+    if (!live) return -INFINITY;
     if (done) {
       v = (unsigned)eos;
-      return at == 0 ? (double)sc : -INFINITY;
+      return at == 0 ? sc : -INFINITY;
     }
-    const unsigned long long k = at < n_out ? keys[row * n_out + at] : 0;
+    const unsigned long long k = at < n_out ? s_list[lane][at] : 0;
     if (!k) return -INFINITY;
     v = beam_key_index(k);
-    return ((double)beam_key_logit(k) - base) + (double)sc;
+    return ((double)beam_key_logit(k) - base) + sc;
   };
   unsigned v = 0;
   double c = value(v);
-  __syncwarp();
   for (int n = 0; n < n_out; ++n) {
     // the lane with the largest c (the lowest lane of equal ones: beams are in
     // lane order, so that is the lowest k V + v)
@@ -136,8 +306,7 @@ __global__ void __launch_bounds__(32)
       }
     }
     const long long o = (long long)blockIdx.x * n_out + n;
-    const bool none = !(m > -INFINITY);
-    if (none) {
+    if (!(m > -INFINITY)) {
       if (lane == 0) {
         out_scores[o] = -INFINITY;
         parent[o] = n % beams;
