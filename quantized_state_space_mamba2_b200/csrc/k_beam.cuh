@@ -24,7 +24,8 @@ constexpr int kBeamMax = 32;  // beams and n_out
 constexpr int kBeamThreads = 256;
 
 // One candidate as a 64-bit key whose order is (larger logit, lower index):
-// the fp32 bits made monotone above the complement of the index.  0: none.
+// the fp32 bits made monotone above the complement of the index.  0: none.  (l
+// is not -0: the caller adds 0, so that equal values tie.)
 __device__ __forceinline__ unsigned long long beam_key(float l, unsigned v) {
   const unsigned b = __float_as_uint(l);
   const unsigned m = b & 0x80000000u ? ~b : b | 0x80000000u;
@@ -38,10 +39,9 @@ __device__ __forceinline__ unsigned beam_key_index(unsigned long long k) {
   return 0xFFFFFFFFu - (unsigned)k;
 }
 
-// NaN counts as -inf, +inf as the largest finite value; -0 as 0 (equal values
-// must tie)
+// NaN counts as -inf, +inf as the largest finite value
 __device__ __forceinline__ float beam_logit(float l) {
-  return fminf(fmaxf(l, -INFINITY), 3.402823466e38f) + 0.0f;
+  return fminf(fmaxf(l, -INFINITY), 3.402823466e38f);
 }
 constexpr int kBeamCap = 512;
 
@@ -88,16 +88,16 @@ struct BeamChunk {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (sizeof(T) == 4) {
-            v[4 * j + i] = beam_logit(__uint_as_float(w[i]));
+            v[4 * j + i] = __uint_as_float(w[i]);
           } else {
-            v[8 * j + 2 * i] = beam_logit(__uint_as_float(w[i] << 16));
-            v[8 * j + 2 * i + 1] = beam_logit(__uint_as_float(w[i] & 0xFFFF0000u));
+            v[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
+            v[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
           }
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-          v[kVec * j + i] = p + i < V ? beam_logit((float)row[p + i]) : -INFINITY;
+          v[kVec * j + i] = p + i < V ? (float)row[p + i] : -INFINITY;
       }
     }
   }
@@ -123,16 +123,18 @@ __device__ __forceinline__ unsigned long long cta_max_key(unsigned long long k,
 // [rows, S] (the chunk's maximum) and sum [rows, S] (of exp(l - top)).
 // A row that cannot win by its logits -- its beam finished or dead -- is not read.
 template <typename T, int E>
-__global__ void __launch_bounds__(kBeamThreads)
+__global__ void __launch_bounds__(kBeamThreads, E == 32 ? 4 : 6)
     k_beam_chunks(const T *__restrict__ logits, long long ld, unsigned V, int S, int n_out,
                   const float *__restrict__ scores, const uint8_t *__restrict__ finished,
                   unsigned long long *__restrict__ keys, float *__restrict__ tops,
                   double *__restrict__ sums) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_group[32];
+  constexpr int kVec = BeamChunk<T, E>::kVec, kGroups = E / kVec;
+  __shared__ float4 s_max[kBeamThreads / 4];
   __shared__ double s_sum[kBeamThreads / 32];
   __shared__ unsigned long long s_key[kBeamCap];
+  __shared__ float s_bar;
   __shared__ int s_count;
   const unsigned row = blockIdx.x / S, chunk = blockIdx.x - row * S;
   if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
@@ -140,38 +142,72 @@ __global__ void __launch_bounds__(kBeamThreads)
   if (threadIdx.x == 0) s_count = 0;
   BeamChunk<T, E> c;
   c.load(logits + (long long)row * ld, V, chunk);
-  float m = c.v[0];
+  float gm[kGroups], top, sum;
+  // maxima of the thread's 16-byte groups and of the chunk (NaN counts as
+  // nothing there), then the sum
+  auto maxima = [&]() {
+    float m = -INFINITY;
 #pragma unroll
-  for (int i = 1; i < E; ++i) m = fmaxf(m, c.v[i]);
+    for (int j = 0; j < kGroups; ++j) {
+      gm[j] = c.v[j * kVec];
 #pragma unroll
-  for (int o = 1; o <= 4; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((lane & 7) == 0) s_group[threadIdx.x >> 3] = m;
-  __syncthreads();
-  // every warp: the chunk's maximum and the n-th largest group maximum
-  const float g = s_group[lane];
-  const float top = warp_max(g);
-  int rank = 0;
+      for (int i = 1; i < kVec; ++i) gm[j] = fmaxf(gm[j], c.v[j * kVec + i]);
+      m = fmaxf(m, gm[j]);
+    }
+    reinterpret_cast<float *>(s_max)[threadIdx.x] = m;
+    __syncthreads();
+    const float4 x = s_max[2 * lane], y = s_max[2 * lane + 1];
+    const float g = fmaxf(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)),
+                          fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w)));  // of threads 8 lane .. + 7
+    top = warp_max(g);
+    return g;
+  };
+  auto exponentials = [&]() {
+    sum = 0.0f;
+    if (top > -INFINITY) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const float o = __shfl_sync(0xffffffffu, g, j);
-    rank += o > g || (o == g && j < lane);
-  }
-  const float bar = __shfl_sync(0xffffffffu, g, __ffs(__ballot_sync(0xffffffffu, rank == n_out - 1)) - 1);
-  float sum = 0.0f;
-  if (top > -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      sum += exp2f((c.v[i] - top) * 1.4426950408889634f);
-      if (c.v[i] >= bar && c.v[i] > -INFINITY) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kBeamCap) s_key[at] = beam_key(c.v[i], c.at(i));
+      for (int i = 0; i < E; ++i) {
+        float e;  // exp(l - top), within 2^-22 and the argument's rounding
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((c.v[i] - top) * 1.4426950408889634f));
+        sum += e;
       }
     }
+  };
+  float g = maxima();
+  exponentials();
+  if (__syncthreads_or(!(sum < INFINITY))) {
+    // a NaN, or +inf as the maximum: the values the definition gives them
+#pragma unroll
+    for (int i = 0; i < E; ++i) c.v[i] = beam_logit(c.v[i]);
+    g = maxima();
+    exponentials();
+  }
+  if (warp == 0) {
+    // the n-th largest group maximum; values of -inf are no candidates
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float o = __shfl_sync(0xffffffffu, g, j);
+      rank += o > g || (o == g && j < lane);
+    }
+    if (rank == n_out - 1) s_bar = fmaxf(g, -3.402823466e38f);
   }
   double total = (double)sum;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) s_sum[warp] = total;
+  __syncthreads();
+  const float bar = s_bar;
+#pragma unroll
+  for (int j = 0; j < kGroups; ++j)
+    if (gm[j] >= bar) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (c.v[j * kVec + i] >= bar) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kBeamCap) s_key[at] = beam_key(c.v[j * kVec + i] + 0.0f, c.at(j * kVec + i));
+        }
+    }
   __syncthreads();
   unsigned long long *out = keys + (size_t)blockIdx.x * n_out;
   const int count = s_count;
@@ -199,7 +235,7 @@ __global__ void __launch_bounds__(kBeamThreads)
     unsigned long long best = 0;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      const unsigned long long k = c.v[i] > -INFINITY ? beam_key(c.v[i], c.at(i)) : 0;
+      const unsigned long long k = c.v[i] > -INFINITY ? beam_key(c.v[i] + 0.0f, c.at(i)) : 0;
       if (k < last && k > best) best = k;
     }
     last = cta_max_key(best, s_key);
