@@ -64,7 +64,7 @@ struct BeamChunk {
     first = chunk * (unsigned)(kBeamThreads * E) + threadIdx.x * kVec;
 #pragma unroll
     for (int j = 0; j < E / kVec; ++j) {
-      const unsigned long long p = (unsigned long long)first + j * (kBeamThreads * kVec);
+      const unsigned p = first + j * (kBeamThreads * kVec);  // V < 2^31
       if (p + 2 * kVec <= V) {
         const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row + p) - skew);
         const uint4 x = q[0];
