@@ -10,9 +10,17 @@ template <typename TX>
 static fm_status launch_add_norm(const void *x, int64_t ldx, const float *residual, int64_t ldr,
                                  int64_t M, int K, const float *w, double eps, bool e4m3, void *q,
                                  float *s, float *sum, int64_t lds, cudaStream_t st) {
-  auto kern = e4m3 ? k_add_norm_quant<TX, true> : k_add_norm_quant<TX, false>;
-  FM_TRY(launch_ex("k_add_norm_quant", kern, (unsigned)M, 32 * ((K + kNormCols - 1) / kNormCols), 0,
-                   st, (const TX *)x, (long long)ldx, residual, (long long)ldr, K, w, eps,
+  const int threads = 32 * ((K + kNormCols - 1) / kNormCols);
+  const bool ahead = K <= kNormAheadK;
+  auto kern = ahead ? (e4m3 ? k_add_norm_quant<TX, true, true> : k_add_norm_quant<TX, false, true>)
+                    : (e4m3 ? k_add_norm_quant<TX, true, false> : k_add_norm_quant<TX, false, false>);
+  // as many CTAs as an SM holds (the kernel that fetches ahead: 640 threads'
+  // registers), each with a row ahead, or one per row
+  const int64_t grid = ahead ? std::min<int64_t>(M, (int64_t)sm_count() *
+                                                        std::min(32, 640 / threads))
+                             : M;
+  FM_TRY(launch_ex("k_add_norm_quant", kern, (unsigned)grid, threads, 0, st, (const TX *)x,
+                   (long long)ldx, residual, (long long)ldr, (long long)M, K, 1.0 / (double)K, w, eps,
                    (uint8_t *)q, s, sum, (long long)lds));
   return launched("k_add_norm_quant");
 }

@@ -4,6 +4,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+#include <type_traits>
 #include "fm_common.cuh"
 
 namespace fm {
@@ -45,15 +46,24 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 // between two codes that its rounding could, and that element is then redone
 // in 64 bits), so they do not depend on the order of any fp32 sum.
 //
-// One CTA per row, one warp per 512 columns: 8 lanes hold a 128-column block,
+// A CTA walks rows, one warp per 512 columns: 8 lanes hold a 128-column block,
 // lane l of them the four groups of 4 columns at 4 l + 32 j, so every load of
 // the 8 lanes is one run of 128 bytes (fp32) and a block's maximum takes three
-// shuffles.  The row stays in registers: one read of x, residual and w, one
-// write of the sum, the codes and the scales.
+// shuffles.  A row stays in registers: one read of x and residual, one write of
+// the sum, the codes and the scales; the weights are read once per CTA.  Up to
+// kNormAheadK columns the next row is on its way while this one is computed
+// (8192 x 2560 fp32 with residual: 63.5 us without, 4.3 TB/s, each row's loads
+// waited for by themselves).
 constexpr int kNormCols = 512;   // columns per warp
 constexpr int kNormMaxK = 32 * kNormCols;
+constexpr int kNormAheadWarps = 10, kNormAheadK = kNormAheadWarps * kNormCols;
 constexpr float kNormTiny = 7.888609052210118e-31f;  // 2^-100: a smaller max|y| counts as zero
 
+__device__ __forceinline__ uint32_t group8_max(uint32_t v) {
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
 __device__ __forceinline__ float group8_max(float v) {
 #pragma unroll
   for (int o = 4; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -62,138 +72,194 @@ __device__ __forceinline__ float group8_max(float v) {
 
 // v = r w c in 64 bits, rounded to fp32 towards zero with the lost bits kept as
 // a last 1: a later rounding to fewer than 22 bits is then that of v itself
-__device__ __forceinline__ float sticky_product(float r, float w, double c) {
-  const double v = __dmul_rn(__dmul_rn((double)r, (double)w), c);
+__device__ __forceinline__ float sticky(double v) {
   float f = __double2float_rz(v);
   if ((double)f != v) f = __uint_as_float(__float_as_uint(f) | 1u);
   return f;
 }
+__device__ __forceinline__ float sticky_product(float r, float w, double c) {
+  return sticky(__dmul_rn(__dmul_rn((double)r, (double)w), c));
+}
 
-// e4m3: t = p cf is within 3 ulp of y / s.  A tie of two codes has the low 20
-// of its 23 fraction bits at 0x80000; below the normal codes (|t| < 2^-6) and
-// not under half the smallest one (2^-10) the spacing is fixed, and the few
-// values there are always redone.
-__device__ __forceinline__ float e4m3_arg(float p, float cf, float r, float w, double c) {
-  float t = __fmul_rn(p, cf);
+// Whether t, within 4 ulp of y / s, may round to another code than it does:
+// e4m3: a tie of two codes has the low 20 of its 23 fraction bits at 0x80000;
+// below the normal codes (|t| < 2^-6) and not under half the smallest one
+// (2^-10) the spacing is fixed, and the few values there are always redone.
+__device__ __forceinline__ bool e4m3_near(float t) {
   const uint32_t a = __float_as_uint(t) & 0x7FFFFFFFu;
-  if ((a & 0xFFFFFu) - 0x7FFF8u <= 16u || a - 0x3A7FF000u < 0x3C800000u - 0x3A7FF000u)
-    t = sticky_product(r, w, c);
-  return t;
+  return (a & 0xFFFFFu) - 0x7FFF8u <= 16u || a - 0x3A7FF000u < 0x3C800000u - 0x3A7FF000u;
 }
-// int8: t = p cf is within 127 * 3 * 2^-24 < 2^-15 of y / s
-__device__ __forceinline__ int int8_code(float p, float cf, float r, float w, double c) {
-  float t = __fmul_rn(p, cf);
-  if (fabsf(__fsub_rn(t, rintf(t))) > 0.5f - 0x1p-14f) t = sticky_product(r, w, c);
-  return quant127(t);
+// int8: |y / s| <= 127, so t is within 127 * 4 * 2^-24 < 2^-15 of it
+__device__ __forceinline__ bool int8_near(float t) {
+  return fabsf(__fsub_rn(t, rintf(t))) > 0.5f - 0x1p-14f;
 }
 
-template <typename TX, bool E4M3>
-__global__ void __launch_bounds__(1024) k_add_norm_quant(
-    const TX *x, long long ldx, const float *residual, long long ldr, int K,
-    const float *__restrict__ norm_w, double eps, uint8_t *__restrict__ q, float *__restrict__ s,
-    float *sum_out, long long lds) {
+// four elements of a row in their stored type
+struct NormRaw4f {
+  float4 v;
+  __device__ __forceinline__ void load(const float *p) { v = load4(p); }
+  __device__ __forceinline__ float4 f32() const { return v; }
+};
+struct NormRaw4b {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    u = *reinterpret_cast<const uint2 *>(p);
+  }
+  __device__ __forceinline__ float4 f32() const {
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+  }
+};
+template <typename TX>
+using NormRaw = std::conditional_t<sizeof(TX) == 4, NormRaw4f, NormRaw4b>;
+
+template <typename TX, bool E4M3, bool kAhead>
+__global__ void __launch_bounds__(kAhead ? 32 * kNormAheadWarps : 1024, kAhead ? 2 : 1)
+    k_add_norm_quant(const TX *x, long long ldx, const float *residual, long long ldr, long long M,
+                     int K, double inv_k, const float *__restrict__ norm_w, double eps,
+                     uint8_t *__restrict__ q, float *__restrict__ s, float *sum_out,
+                     long long lds) {
   pdl_wait();
   pdl_trigger();
-  __shared__ double s_ss[32];
-  __shared__ float s_max[32], s_rem[32];
-  const long long row = blockIdx.x;
+  // by the row's parity: a warp is never more than one row ahead of another
+  __shared__ double s_ss[2][32];
+  __shared__ uint32_t s_max[2][32];
+  __shared__ float s_rem[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   const int col0 = warp * kNormCols + (lane >> 3) * 128 + (lane & 7) * 4;
-  float r[16], w[16];
+  float w[16];
+  if constexpr (kAhead) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = col0 + 32 * j;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v, g = v;
-    if (c < K) {
-      v = load4(x + row * ldx + c);
-      if (residual) u = load4(residual + row * ldr + c);
-      g = load4(norm_w + c);
+    for (int j = 0; j < 4; ++j) {
+      const int c = col0 + 32 * j;
+      const float4 g = c < K ? load4(norm_w + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      w[4 * j] = g.x; w[4 * j + 1] = g.y; w[4 * j + 2] = g.z; w[4 * j + 3] = g.w;
     }
-    if (residual) {
-      v.x = __fadd_rn(v.x, u.x); v.y = __fadd_rn(v.y, u.y);
-      v.z = __fadd_rn(v.z, u.z); v.w = __fadd_rn(v.w, u.w);
+  }
+  NormRaw<TX> nx[4];
+  float4 nr[4];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = col0 + 32 * j;
+      if (c < K) {
+        nx[j].load(x + row * ldx + c);
+        if (residual) nr[j] = load4(residual + row * ldr + c);
+      } else {
+        nx[j] = {};
+        nr[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
-    r[4 * j] = v.x; r[4 * j + 1] = v.y; r[4 * j + 2] = v.z; r[4 * j + 3] = v.w;
-    w[4 * j] = g.x; w[4 * j + 1] = g.y; w[4 * j + 2] = g.z; w[4 * j + 3] = g.w;
-    if (sum_out && c < K) *reinterpret_cast<float4 *>(sum_out + row * lds + c) = v;
-  }
-  double ss = 0.0;
+  };
+  if (kAhead) fetch(blockIdx.x);
+  int odd = 0;
+  for (long long row = blockIdx.x; row < M; row += gridDim.x, odd ^= 1) {
+    if (!kAhead) fetch(row);
+    float r[16];
+    double ss = 0.0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ss = __fma_rn((double)r[i], (double)r[i], ss);
+    for (int j = 0; j < 4; ++j) {
+      float4 v = nx[j].f32();
+      if (residual) {
+        v.x = __fadd_rn(v.x, nr[j].x); v.y = __fadd_rn(v.y, nr[j].y);
+        v.z = __fadd_rn(v.z, nr[j].z); v.w = __fadd_rn(v.w, nr[j].w);
+      }
+      const int c = col0 + 32 * j;
+      if (sum_out && c < K) *reinterpret_cast<float4 *>(sum_out + row * lds + c) = v;
+      r[4 * j] = v.x; r[4 * j + 1] = v.y; r[4 * j + 2] = v.z; r[4 * j + 3] = v.w;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-  if (lane == 0) s_ss[warp] = ss;
-  __syncthreads();
-  ss = lane < nw ? s_ss[lane] : 0.0;
+      for (int i = 0; i < 4; ++i) ss = __fma_rn((double)r[4 * j + i], (double)r[4 * j + i], ss);
+      if constexpr (!kAhead) {
+        const float4 g = c < K ? load4(norm_w + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        w[4 * j] = g.x; w[4 * j + 1] = g.y; w[4 * j + 2] = g.z; w[4 * j + 3] = g.w;
+      }
+    }
+    if (kAhead && row + gridDim.x < M) fetch(row + gridDim.x);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-  if (!(ss <= 1.7e308) && threadIdx.x == 0) raise_error(kErrNonfinite);
-  const double rstd = __drcp_rn(__dsqrt_rn(__dadd_rn(__ddiv_rn(ss, (double)K), eps)));
-  // rstd = rs 2^e with rs in [1, 2): r 2^e is exact and at most about sqrt(K),
-  // so the products below cannot overflow whatever the row's magnitude
-  const long long rb = __double_as_longlong(rstd);
-  const int e = (int)((rb >> 52) & 0x7FF) - 1023;
-  const double rs = __longlong_as_double((rb & 0xFFFFFFFFFFFFFll) | 0x3FF0000000000000ll);
-  const float pe = ldexpf(1.0f, e);
-  float p[16], m = 0.0f;
-  bool finite = true;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    r[i] = __fmul_rn(r[i], pe);
-    p[i] = __fmul_rn(r[i], w[i]);
-    finite = finite && fabsf(p[i]) <= 3.402823466e38f;
-    m = fmaxf(m, fabsf(p[i]));
-  }
-  if (!finite) raise_error(kErrNonfinite);
-  // max|r w| exactly: the largest fp32 product plus the largest exact
-  // remainder among the elements that round to it
-  m = group8_max(m);
-  if (!E4M3) {
-    m = warp_max(m);
-    if (lane == 0) s_max[warp] = m;
+    for (int o = 16; o >= 1; o >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+    if (lane == 0) s_ss[odd][warp] = ss;
     __syncthreads();
-    m = warp_max(lane < nw ? s_max[lane] : 0.0f);
-  }
-  float rem = -3.0e38f;
+    ss = s_ss[odd][0];
+    for (int i = 1; i < nw; ++i) ss = __dadd_rn(ss, s_ss[odd][i]);
+    if (!(ss <= 1.7e308) && threadIdx.x == 0) raise_error(kErrNonfinite);
+    const double rstd = rsqrt(__fma_rn(ss, inv_k, eps));
+    // rstd = rs 2^e with rs in [1, 2): r 2^e is exact and at most about sqrt(K),
+    // so the products below cannot overflow whatever the row's magnitude
+    const long long rb = __double_as_longlong(rstd);
+    const int e = (int)((rb >> 52) & 0x7FF) - 1023;
+    const double rs = __longlong_as_double((rb & 0xFFFFFFFFFFFFFll) | 0x3FF0000000000000ll);
+    const float pe = e >= -126 && e <= 127 ? __int_as_float((127 + e) << 23) : ldexpf(1.0f, e);
+    float p[16];
+    uint32_t mb = 0;  // bits of the largest |p|: ordered as the values, NaN above all
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (fabsf(p[i]) == m) rem = fmaxf(rem, __fmaf_rn(fabsf(r[i]), fabsf(w[i]), -m));
-  rem = group8_max(rem);
-  if (!E4M3) {
-    rem = warp_max(rem);
-    if (lane == 0) s_rem[warp] = rem;
-    __syncthreads();
-    rem = warp_max(lane < nw ? s_rem[lane] : -3.0e38f);
-  }
-  double amax = __dmul_rn(__dadd_rn((double)m, (double)rem), rs);
-  // below 2^-100 (which covers every p that lost bits to underflow): zeros
-  if (!(m > 0.0f) || amax < (double)kNormTiny) amax = 0.0;
-  const float sc = (float)__ddiv_rn(amax, E4M3 ? 448.0 : 127.0);
-  const double c = sc > 0.0f ? __ddiv_rn(rs, (double)sc) : 0.0;
-  const float cf = (float)c;
+    for (int i = 0; i < 16; ++i) {
+      r[i] = __fmul_rn(r[i], pe);
+      p[i] = __fmul_rn(r[i], w[i]);
+      mb = max(mb, __float_as_uint(p[i]) & 0x7FFFFFFFu);
+    }
+    // max|r w| exactly: the largest fp32 product plus the largest exact
+    // remainder among the elements that round to it
+    mb = group8_max(mb);
+    if (!E4M3) {
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 8));
+      mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 16));
+      if (lane == 0) s_max[odd][warp] = mb;
+      __syncthreads();
+      mb = s_max[odd][0];
+      for (int i = 1; i < nw; ++i) mb = max(mb, s_max[odd][i]);
+    }
+    if (mb >= 0x7F800000u) raise_error(kErrNonfinite);
+    const float m = __uint_as_float(mb);
+    float rem = -3.0e38f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int col = col0 + 32 * j;
-    uint32_t o;
-    if constexpr (E4M3) {
+    for (int i = 0; i < 16; ++i)
+      if (fabsf(p[i]) == m) rem = fmaxf(rem, __fmaf_rn(fabsf(r[i]), fabsf(w[i]), -m));
+    rem = group8_max(rem);
+    if (!E4M3) {
+      rem = fmaxf(rem, __shfl_xor_sync(0xffffffffu, rem, 8));
+      rem = fmaxf(rem, __shfl_xor_sync(0xffffffffu, rem, 16));
+      if (lane == 0) s_rem[odd][warp] = rem;
+      __syncthreads();
+      rem = s_rem[odd][0];
+      for (int i = 1; i < nw; ++i) rem = fmaxf(rem, s_rem[odd][i]);
+    }
+    double amax = __dmul_rn(__dadd_rn((double)m, (double)rem), rs);
+    // below 2^-100 (which covers every p that lost bits to underflow): zeros
+    if (!(m > 0.0f) || amax < (double)kNormTiny) amax = 0.0;
+    const float sc = (float)__dmul_rn(amax, E4M3 ? 1.0 / 448.0 : 1.0 / 127.0);
+    const float cf = sc > 0.0f ? __fdiv_rn((float)rs, sc) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = col0 + 32 * j;
       float t[4];
+      bool near = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        t[i] = e4m3_arg(p[4 * j + i], cf, r[4 * j + i], w[4 * j + i], c);
-      o = e4m3x2(t[0], t[1]) | (e4m3x2(t[2], t[3]) << 16);
-    } else {
-      o = 0;
+      for (int i = 0; i < 4; ++i) {
+        t[i] = __fmul_rn(p[4 * j + i], cf);
+        near = near || (E4M3 ? e4m3_near(t[i]) : int8_near(t[i]));
+      }
+      if (near && sc > 0.0f) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o |= (uint32_t)(int8_code(p[4 * j + i], cf, r[4 * j + i], w[4 * j + i], c) & 0xFF) << (8 * i);
+        for (int i = 0; i < 4; ++i)
+          t[i] = sticky(__ddiv_rn(
+              __dmul_rn(__dmul_rn((double)r[4 * j + i], (double)w[4 * j + i]), rs), (double)sc));
+      }
+      uint32_t o;
+      if constexpr (E4M3) {
+        o = e4m3x2(t[0], t[1]) | (e4m3x2(t[2], t[3]) << 16);
+      } else {
+        o = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o |= (uint32_t)(quant127(t[i]) & 0xFF) << (8 * i);
+      }
+      if (col < K) *reinterpret_cast<uint32_t *>(q + row * K + col) = o;
     }
-    if (col < K) *reinterpret_cast<uint32_t *>(q + row * K + col) = o;
-  }
-  if constexpr (E4M3) {
-    const int nb = (K + 127) / 128, b = warp * 4 + (lane >> 3);
-    if ((lane & 7) == 0 && b < nb) s[row * nb + b] = sc;
-  } else {
-    if (threadIdx.x == 0) s[row] = sc;
+    if constexpr (E4M3) {
+      const int nb = (K + 127) / 128, b = warp * 4 + (lane >> 3);
+      if ((lane & 7) == 0 && b < nb) s[row * nb + b] = sc;
+    } else {
+      if (threadIdx.x == 0) s[row] = sc;
+    }
   }
 }
 
