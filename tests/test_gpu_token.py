@@ -224,6 +224,26 @@ def test_product_large(lib):
     check_product(lib, *product_case(g, 48, 50000, 768, 0.3), torch.empty(48, 50000, device="cuda"))
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 1000, 768), (100, 5000, 400), (300, 3000, 2560), (2500, 2700, 640)])
+def test_product_reports_a_wait_that_gave_up(lib, M, N, K):
+    """Loads that are never issued: the waits run out after 20 ms, the call ends
+    and says so, and the next one is right (every kernel variant)."""
+    g = gen(K)
+    case = product_case(g, M, N, K, 0.3)
+    y = torch.empty(M, N, device="cuda")
+    lib.sync_status()
+    lib.set_fault_injection(lib.STALL_GEMM, 20_000_000)
+    try:
+        lib.fp8_gemm(*case, y)
+        torch.cuda.synchronize()
+    finally:
+        lib.set_fault_injection(0, 0)
+    with pytest.raises(lib.FmError) as e:
+        lib.sync_status()
+    assert e.value.status == 6
+    check_product(lib, *case, y)
+
+
 # ------------------------------------------------------------------ embedding rows
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "e4m3"])
 @pytest.mark.parametrize("M,V,K", [(1, 1, 16), (7, 130, 144), (64, 1000, 2560), (300, 257, 768),
