@@ -177,11 +177,10 @@ extern "C" fm_status fm_fp8_gemm(const void *A, const float *s_a, int64_t M, con
 }
 
 // ------------------------------------------------------------------ beam selection
-// Logits per thread of a chunk: 32 where that gives two CTAs per SM (of 148),
-// fewer for the latency of small selections.
+// Logits per thread of a chunk: 16, or 8 for the latency of selections that
+// would give an SM (of 148) less than two chunks of 16.
 static int beam_elems(int64_t rows, int64_t V) {
-  const auto ctas = [&](int e) { return rows * ((V + kBeamThreads * e - 1) / (kBeamThreads * e)); };
-  return ctas(32) >= 296 ? 32 : ctas(16) >= 296 ? 16 : 8;
+  return rows * ((V + kBeamThreads * 16 - 1) / (kBeamThreads * 16)) >= 296 ? 16 : 8;
 }
 static int64_t beam_chunks(int64_t rows, int64_t V) {
   const int64_t n = kBeamThreads * beam_elems(rows, V);
@@ -240,7 +239,7 @@ extern "C" fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t l
   cudaStream_t st = (cudaStream_t)stream;
   auto go = [&](auto t) -> fm_status {
     using T = decltype(t);
-    auto kern = E == 32 ? k_beam_chunks<T, 32> : E == 16 ? k_beam_chunks<T, 16> : k_beam_chunks<T, 8>;
+    auto kern = E == 16 ? k_beam_chunks<T, 16> : k_beam_chunks<T, 8>;
     return launch_ex("k_beam_chunks", kern, (unsigned)chunks, kBeamThreads, 0, st,
                      (const T *)logits, (long long)ld, (unsigned)V, S, n_out, scores, finished, keys,
                      tops, sums);

@@ -9,7 +9,12 @@
 // its n largest logits; k_beam_merge joins the chunks' sums and lists and takes
 // the n best of the beams' lists, by c in 64 bits.
 //
-// The reading is bound by memory.  The n largest of a chunk are found without
+// What bounds it is the chain of each chunk (its loads, the maxima, the sum, the
+// few candidates), so an SM holds as many chunks as its 64 warps allow: 16
+// logits per thread, 8 CTAs.  64 x 8 x 100003 bf16, a fifth of the beams
+// finished: 55.6 us, 1.9 TB/s of logits (32 per thread, 4 CTAs: 61.7; 8 per
+// thread: 88; a warp by itself over a span of the row, without barriers: 73, its
+// code and registers too large).  The n largest of a chunk are found without
 // sorting it: the n-th largest of 32 group maxima (groups of 8 threads) is not
 // above the chunk's n-th largest value, so few values reach it; they are
 // collected and ranked against each other.  Where ties or masks let more than
@@ -123,7 +128,7 @@ __device__ __forceinline__ unsigned long long cta_max_key(unsigned long long k,
 // [rows, S] (the chunk's maximum) and sum [rows, S] (of exp(l - top)).
 // A row that cannot win by its logits -- its beam finished or dead -- is not read.
 template <typename T, int E>
-__global__ void __launch_bounds__(kBeamThreads, E == 32 ? 4 : 6)
+__global__ void __launch_bounds__(kBeamThreads, 8)
     k_beam_chunks(const T *__restrict__ logits, long long ld, unsigned V, int S, int n_out,
                   const float *__restrict__ scores, const uint8_t *__restrict__ finished,
                   unsigned long long *__restrict__ keys, float *__restrict__ tops,
@@ -137,7 +142,9 @@ __global__ void __launch_bounds__(kBeamThreads, E == 32 ? 4 : 6)
   __shared__ float s_bar;
   __shared__ int s_count;
   const unsigned row = blockIdx.x / S, chunk = blockIdx.x - row * S;
-  if ((finished && finished[row]) || !(scores[row] > -INFINITY)) return;
+  const float score = scores[row];  // both loads on their way at once
+  const uint8_t done = finished ? finished[row] : 0;
+  if (done | !(score > -INFINITY)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s_count = 0;
   BeamChunk<T, E> c;
