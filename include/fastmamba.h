@@ -679,8 +679,9 @@ fm_status fm_embed_rows(const int32_t *ids, int64_t M, const void *table, fm_dty
  * n_out = beams.  beams and n_out in [1, 32]; n_out = beams = 1 is greedy
  * decoding; beams = 1 with n_out > 1 opens a search.
  * ws: device workspace of fm_beam_workspace_bytes(B, beams, V, n_out) bytes
- * (0 for invalid sizes), written before it is read.  The logits of a beam that
- * is finished or dead are not read. */
+ * (0 for invalid sizes), written before it is read; calls that may overlap on
+ * the GPU (other streams, other captured graphs) need one each.  The logits of
+ * a beam that is finished or dead are not read. */
 size_t fm_beam_workspace_bytes(int B, int beams, int64_t V, int n_out);
 fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t ld, int B, int beams, int64_t V,
                          const float *scores, const uint8_t *finished, int eos, int n_out,

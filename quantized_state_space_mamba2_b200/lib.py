@@ -513,7 +513,11 @@ def _place(stream):
     """(current device, raw stream) of a call: its tensors must be on that device,
     where it is launched."""
     dev = torch.cuda.current_device()
-    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return dev, _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError("stream: a stream of the current device is required")
+    return dev, stream.cuda_stream
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -658,6 +662,17 @@ class RowSet:
             _dense("src", s, s.shape[:1] + d.shape[1:], (d.dtype,), self.device)
         if n and len({(d.shape[0], s.shape[0]) for d, s in zip(self.dst, self.src)}) != 1:
             raise ValueError("RowSet: every buffer must have the same number of rows")
+        # a buffer is written by its own threads only: none may overlap another's
+        # rows, nor the rows that another is read from
+        span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+        used = sorted({span(d) + (i,) for i, d in enumerate(self.dst)}
+                      | {span(s) + (i,) for i, s in enumerate(self.src)})
+        end, owner = 0, None
+        for lo, hi, i in used:
+            if lo < end and hi > lo and owner != i:
+                raise ValueError("RowSet: buffers overlap")
+            if hi > end:
+                end, owner = hi, i
         self.dst_rows, self.src_rows = (self.dst[0].shape[0], self.src[0].shape[0]) if n else (0, 0)
         self._dst = (C.c_void_p * n)(*[t.data_ptr() for t in self.dst])
         self._src = (C.c_void_p * n)(*[t.data_ptr() for t in self.src])

@@ -127,6 +127,9 @@ def test_python_checks(monkeypatch):
     monkeypatch.setattr(lib, "_place", lambda stream: (-1, 0))  # host tensors stand for the device's
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     z, i8, i32, f8 = torch.zeros, torch.int8, torch.int32, torch.float8_e4m3fn
+    whole = z(8, 4)
+    lib.RowSet([whole[:4], whole[4:]])  # neighbours are no overlap
+    lib.RowSet([z(4, 4), z(4, 4)], [whole[:4], whole[4:]])
     refused = [
         ("dtype", lambda: lib.add_norm_quant(z(2, 32, dtype=torch.float16), z(32), z(2, 32, dtype=i8), z(2))),
         ("shape", lambda: lib.add_norm_quant(z(2, 32), z(31), z(2, 32, dtype=i8), z(2))),
@@ -146,6 +149,9 @@ def test_python_checks(monkeypatch):
         ("rows", lambda: lib.reorder_rows(lib.RowSet([z(8, 4)]), z(2, 3, dtype=i32))),
         ("number of rows", lambda: lib.RowSet([z(8, 4), z(6, 4)])),
         ("shape", lambda: lib.RowSet([z(8, 4)], [z(2, 5)])),
+        ("overlap", lambda: lib.RowSet([whole[:4], whole[2:6]])),
+        ("overlap", lambda: lib.RowSet([whole[:4], whole[:4]])),
+        ("overlap", lambda: lib.RowSet([z(4, 4), whole[:4]], [whole[2:6], z(4, 4)])),
     ]
     for i, (why, call) in enumerate(refused):
         with pytest.raises(ValueError, match=why):
