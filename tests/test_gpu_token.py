@@ -505,6 +505,80 @@ def test_another_stream_and_a_replayed_graph(lib):
     lib.sync_status()
 
 
+def test_two_streams_at_once(lib):
+    """Two chains of calls on two streams, each with its own buffers, give the
+    bits of one alone."""
+    g = gen(31)
+    K, V, B, k = 768, 9001, 4, 4
+    t = torch.empty(V, K, device="cuda", dtype=E4M3)
+    ts = torch.empty(P.blocks(V), P.blocks(K), device="cuda")
+    lib.prepare_linear_fp8(0.1 * randn(g, V, K), t, ts)
+    w, x = torch.ones(K, device="cuda"), randn(g, 700, K)
+
+    def chain(reps):
+        e = lambda *s, dtype=torch.float32: torch.zeros(*s, device="cuda", dtype=dtype)
+        q, s = e(700, K, dtype=torch.int8).view(E4M3), e(700, P.blocks(K))
+        y, z, sc = e(700, V), e(16, V), e(B, k)
+        par, tok = e(B, k, dtype=torch.int32), e(B, k, dtype=torch.int32)
+        ws = e(lib.beam_workspace_bytes(B, k, V, k), dtype=torch.uint8)
+        state = torch.arange(B * k * 4096, device="cuda", dtype=torch.int32).view(B * k, 4096)
+        rows = lib.RowSet([state])
+        for _ in range(reps):
+            lib.add_norm_quant(x, w, q, s)
+            lib.fp8_gemm(q, s, t, ts, y)
+            lib.fp8_gemm(q[:16], s[:16], t, ts, z)
+            lib.beam_select(z.view(B, k, V), sc, sc, par, tok, ws)
+            lib.reorder_rows(rows, par)
+        return y, z, sc, par, tok, state
+
+    want = chain(6)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for st in streams:
+        with torch.cuda.stream(st):
+            got.append(chain(6))
+    torch.cuda.synchronize()
+    lib.sync_status()
+    assert all(torch.equal(a, b) for one in got for a, b in zip(one, want))
+
+
+def test_offsets_past_32_bits(lib):
+    g = gen(41)
+    # a table of more than 2^31 elements
+    V, K = 140001, 16384
+    t = torch.zeros(V, K, device="cuda", dtype=torch.bfloat16)
+    t[-1] = randn(g, K).bfloat16()
+    t[7] = randn(g, K).bfloat16()
+    x = torch.empty(3, K, device="cuda")
+    lib.embed_rows(torch.tensor([V - 1, 7, V - 1], device="cuda", dtype=torch.int32), t, x)
+    assert torch.equal(x, t[[V - 1, 7, V - 1]].float())
+    del t
+    # a product with as many outputs, and one with a long row stride
+    M, N = 66001, 33000
+    a, sa, w, sw = product_case(g, M, N, 16, 0.3)
+    y = torch.zeros(M, N, device="cuda", dtype=torch.bfloat16)
+    lib.fp8_gemm(a, sa, w, sw, y)
+    lib.sync_status()
+    want = P.dequant_rows(a[-70:], sa[-70:]) @ P.dequant_blocks(w, sw).t()
+    tol = (want.abs() + 1e-3 * want.abs().mean()) * 2.0 ** -8
+    assert bool(((y[-70:].to(F64) - want).abs() <= tol).all())
+    del y
+    wide = torch.zeros(40, 60_000_000, device="cuda", dtype=torch.bfloat16)
+    lib.fp8_gemm(a[:40], sa[:40], w[:500], sw[:4], wide[:, :500])
+    lib.sync_status()
+    want = P.dequant_rows(a[:40], sa[:40]) @ P.dequant_blocks(w[:500], sw[:4]).t()
+    assert bool(((wide[:, :500].to(F64) - want).abs() <= (want.abs() + 1e-3 * want.abs().mean()) * 2.0 ** -8).all())
+    # logits of as many elements
+    del wide
+    l = torch.zeros(75, 6, 5_000_003, device="cuda", dtype=torch.bfloat16)
+    l[74, 5, 5_000_002] = 9.0
+    l[74, 2, 4_999_000] = 8.0
+    sc = torch.zeros(75, 6, device="cuda")
+    out = select(lib, l, sc, 3)
+    assert out[1][74, :2].tolist() == [5, 2] and out[2][74, :2].tolist() == [5_000_002, 4_999_000]
+    assert out[1][73].tolist() == [0, 0, 0] and out[2][73].tolist() == [0, 1, 2]
+
+
 # ------------------------------------------------------------------ all of them together
 @pytest.fixture(scope="module")
 def model(lib):
