@@ -275,30 +275,35 @@ __global__ void __launch_bounds__(32 * kBeamMax)
   __shared__ uint8_t s_done[kBeamMax];
   const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5;
   const long long row = (long long)blockIdx.x * beams + beam;
+  // every first load on its way at once (what a row that was not read left in
+  // the workspace is loaded too, and not used)
   const float score = scores[row];
-  const bool finish = finished && finished[row], dead = !(score > -INFINITY);
+  const uint8_t flag = finished ? finished[row] : 0;
+  const float *tp = tops + row * S;
+  const double *sp = sums + row * S;
+  const unsigned long long *kp = keys + row * S * n_out;
+  const int all = S * n_out;
+  constexpr int kHold = 8;  // keys per lane held in registers
+  unsigned long long own[kHold], last = ~0ull;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) own[i] = 32 * i + lane < all ? kp[32 * i + lane] : 0;
+  const float top = lane < S ? tp[lane] : -INFINITY;
+  const double sum = lane < S ? sp[lane] : 0.0;
+  const bool finish = flag != 0, dead = !(score > -INFINITY);
   if (lane == 0) {
     s_score[beam] = score;
     s_done[beam] = finish;
   }
   if (!finish && !dead) {
-    const float *tp = tops + row * S;
-    const double *sp = sums + row * S;
-    float m = -INFINITY;
-    for (int i = lane; i < S; i += 32) m = fmaxf(m, tp[i]);
+    float m = top;
+    for (int i = 32 + lane; i < S; i += 32) m = fmaxf(m, tp[i]);
     m = warp_max(m);
-    double t = 0.0;
-    for (int i = lane; i < S; i += 32)
+    double t = sum > 0.0 ? sum * exp((double)top - (double)m) : 0.0;
+    for (int i = 32 + lane; i < S; i += 32)
       if (sp[i] > 0.0) t += sp[i] * exp((double)tp[i] - (double)m);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (lane == 0) s_lse[beam] = (double)m + log(t);
-    const unsigned long long *kp = keys + row * S * n_out;
-    const int all = S * n_out;
-    constexpr int kHold = 8;  // keys per lane held in registers
-    unsigned long long own[kHold], last = ~0ull;
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) own[i] = 32 * i + lane < all ? kp[32 * i + lane] : 0;
     for (int n = 0; n < n_out; ++n) {
       unsigned long long best = 0;
 #pragma unroll
