@@ -333,9 +333,12 @@ extern "C" fm_status fm_embed_rows(const int32_t *ids, int64_t M, const void *ta
                                    float *x, int64_t ldx, fm_stream stream) {
   if (!dtype_in(type, FM_F32, FM_BF16, FM_E4M3))
     return fail(FM_ERR_INVALID_ARG, "%s: the table must be fp32, bf16 or e4m3", __func__);
-  if (M < 0 || (M + 3) / 4 > 0x7FFFFFFF || V < 1 || V > 0x7FFFFFFF || K <= 0 || K % 16 ||
-      K > 0x7FFFFFFF)
+  if (M < 0 || V < 1 || V > 0x7FFFFFFF || K <= 0 || K % 16 || K > 0x7FFFFF00)
     return fail(FM_ERR_SHAPE, "%s: need V in [1, 2^31) and K a positive multiple of 16", __func__);
+  const int64_t pieces = (K + kEmbedCols - 1) / kEmbedCols;
+  if (M > 0x7FFFFFFF / pieces)
+    return fail(FM_ERR_SHAPE, "%s: M=%lld rows of %lld columns are too many", __func__, (long long)M,
+                (long long)K);
   if (ldx < K || ldx % 4)
     return fail(FM_ERR_SHAPE, "%s: ldx must be a multiple of 4, at least K", __func__);
   if (M == 0) return FM_OK;
@@ -344,7 +347,8 @@ extern "C" fm_status fm_embed_rows(const int32_t *ids, int64_t M, const void *ta
   if (type == FM_E4M3) NEED(table_s);
   NEED(x);
   auto kern = type == FM_F32 ? k_embed_rows<0> : type == FM_BF16 ? k_embed_rows<1> : k_embed_rows<2>;
-  FM_TRY(launch_ex("k_embed_rows", kern, (unsigned)((M + 3) / 4), 128, 0, (cudaStream_t)stream, ids,
-                   (long long)M, table, table_s, (long long)V, (int)K, scale, x, (long long)ldx));
+  FM_TRY(launch_ex("k_embed_rows", kern, (unsigned)((M * pieces + 3) / 4), 128, 0,
+                   (cudaStream_t)stream, ids, (long long)M, table, table_s, (long long)V, (int)K,
+                   (int)pieces, scale, x, (long long)ldx));
   return launched("k_embed_rows");
 }

@@ -302,39 +302,52 @@ __global__ void __launch_bounds__(256) k_prepare_linear_fp8(const float *__restr
 
 // ------------------------------------------------------------ embedding rows
 // x[m] = scale * table[ids[m]]; an id of -1 (padding) gives zeros, any other id
-// outside [0, V) zeros and the device error word.  One warp per row.
+// outside [0, V) zeros and the device error word.  One warp per 512 columns of a
+// row, all their loads on their way at once: bound by memory, two thirds of the
+// bytes of a bf16 table's rows being written (8192 x 2560 from bf16: 24.4 us, 5.2
+// TB/s), and by one load's latency where there are few rows (a warp per row, a
+// load per 128 columns after another: 5.1 us for 64 x 2560 in a graph).
 // TYPE 0: fp32 table, 1: bf16, 2: e4m3 codes with a scale per 128 x 128 block.
+constexpr int kEmbedCols = 512;  // columns per warp
+
 template <int TYPE>
 __global__ void __launch_bounds__(128) k_embed_rows(const int32_t *__restrict__ ids, long long M,
                                                     const void *__restrict__ table,
                                                     const float *__restrict__ table_s, long long V,
-                                                    int K, float scale, float *__restrict__ x,
-                                                    long long ldx) {
+                                                    int K, int pieces, float scale,
+                                                    float *__restrict__ x, long long ldx) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const long long row = w / pieces;
   if (row >= M) return;
+  const int c0 = (int)(w - row * pieces) * kEmbedCols + 4 * lane;
   const long long id = ids[row];
   const bool live = id >= 0 && id < V;
-  if (!live && id != -1 && lane == 0) raise_error(kErrIndex);
+  if (!live && id != -1 && c0 == 0) raise_error(kErrIndex);
   const int nb = (K + 127) / 128;
-  for (int c = 4 * lane; c < K; c += 128) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-      if constexpr (TYPE == 0) v = load4((const float *)table + id * K + c);
-      if constexpr (TYPE == 1) v = load4((const __nv_bfloat16 *)table + id * K + c);
+  float4 v[kEmbedCols / 128];
+#pragma unroll
+  for (int j = 0; j < kEmbedCols / 128; ++j) {
+    const int c = c0 + 128 * j;
+    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live && c < K) {
+      if constexpr (TYPE == 0) v[j] = load4((const float *)table + id * K + c);
+      if constexpr (TYPE == 1) v[j] = load4((const __nv_bfloat16 *)table + id * K + c);
       if constexpr (TYPE == 2) {
-        v = e4m3x4_f32(*reinterpret_cast<const uint32_t *>((const uint8_t *)table + id * K + c));
+        v[j] = e4m3x4_f32(*reinterpret_cast<const uint32_t *>((const uint8_t *)table + id * K + c));
         const float s = table_s[(id >> 7) * nb + (c >> 7)];
-        v.x = __fmul_rn(v.x, s); v.y = __fmul_rn(v.y, s);
-        v.z = __fmul_rn(v.z, s); v.w = __fmul_rn(v.w, s);
+        v[j].x = __fmul_rn(v[j].x, s); v[j].y = __fmul_rn(v[j].y, s);
+        v[j].z = __fmul_rn(v[j].z, s); v[j].w = __fmul_rn(v[j].w, s);
       }
-      v.x = __fmul_rn(v.x, scale); v.y = __fmul_rn(v.y, scale);
-      v.z = __fmul_rn(v.z, scale); v.w = __fmul_rn(v.w, scale);
+      v[j].x = __fmul_rn(v[j].x, scale); v[j].y = __fmul_rn(v[j].y, scale);
+      v[j].z = __fmul_rn(v[j].z, scale); v[j].w = __fmul_rn(v[j].w, scale);
     }
-    *reinterpret_cast<float4 *>(x + row * ldx + c) = v;
   }
+#pragma unroll
+  for (int j = 0; j < kEmbedCols / 128; ++j)
+    if (c0 + 128 * j < K) *reinterpret_cast<float4 *>(x + row * ldx + c0 + 128 * j) = v[j];
 }
 
 // ------------------------------------------------------------ state reordering
