@@ -12,7 +12,7 @@
 // What bounds it is the chain of each chunk (its loads, the maxima, the sum, the
 // few candidates), so an SM holds as many chunks as its 64 warps allow: 16
 // logits per thread, 8 CTAs.  64 x 8 x 100003 bf16, a fifth of the beams
-// finished: 55.6 us, 1.9 TB/s of logits (32 per thread, 4 CTAs: 61.7; 8 per
+// finished: 53.6 us, 1.9 TB/s of logits (32 per thread, 4 CTAs: 61.7; 8 per
 // thread: 88; a warp by itself over a span of the row, without barriers: 73, its
 // code and registers too large).  The n largest of a chunk are found without
 // sorting it: the n-th largest of 32 group maxima (groups of 8 threads) is not

@@ -271,6 +271,21 @@ def test_embed(lib, M, V, K, kind):
     assert torch.equal(buf[:, :K], want) and bool((buf[:, K:] == 5.0).all())
 
 
+def test_a_stream_argument(lib):
+    """stream= queues the call there: behind what that stream has been given."""
+    side = torch.cuda.Stream()
+    t = torch.zeros(8, 4096, device="cuda")
+    ids = torch.arange(8, device="cuda", dtype=torch.int32)
+    x = torch.full((8, 4096), -1.0, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for v in range(200):
+            t.fill_(float(v))
+    lib.embed_rows(ids, t, x, stream=side)
+    side.synchronize()
+    assert bool((x == 199.0).all())
+
+
 @pytest.mark.parametrize("bad", [-2, 40, 2 ** 31 - 1, -2 ** 31])
 def test_embed_reports_bad_ids(lib, bad):
     t = torch.ones(40, 32, device="cuda")
