@@ -150,7 +150,7 @@ extern "C" fm_status fm_sync_status(fm_stream stream) {
     FM_CHECK_CUDA(cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)));
     if (word & kErrTimeout) return fail(FM_ERR_TIMEOUT, "a bounded device wait gave up");
     if (word & kErrNonfinite)
-      return fail(FM_ERR_NONFINITE, "a non-finite value (NaN or Inf) reached an int8 quantiser");
+      return fail(FM_ERR_NONFINITE, "a non-finite value (NaN or Inf) reached an 8-bit quantiser");
     if (word & kErrIndex)
       return fail(FM_ERR_INDEX, "a token id or a parent index was out of range");
   }

@@ -165,7 +165,8 @@ def check_product(lib, a, sa, w, sw, y):
 SIZES = [(1, 1, 16), (1, 7, 128), (2, 129, 144), (4, 1001, 768), (15, 33, 256), (16, 128, 128),
          (17, 300, 400), (33, 513, 1040), (64, 2000, 2560), (65, 257, 384), (100, 640, 512),
          (128, 1000, 768), (129, 255, 640), (200, 999, 272), (257, 1537, 1536), (300, 128, 16),
-         (1000, 130, 32), (513, 4097, 144)]
+         (1000, 130, 32), (513, 4097, 144), (7, 300, 8320), (100, 140, 16400), (130, 140, 8336),
+         (20, 20000, 8448)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
