@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kAhead ? 32 * kNormAheadWarps : 1024, kAhead ?
 __global__ void __launch_bounds__(256) k_prepare_linear_fp8(const float *__restrict__ W, long long N,
                                                             int K, uint8_t *__restrict__ Wq,
                                                             float *__restrict__ s_w) {
+  pdl_wait();
   __shared__ float s_red[8];
   const int k0 = blockIdx.x * 128;
   const long long n0 = (long long)blockIdx.y * 128;
