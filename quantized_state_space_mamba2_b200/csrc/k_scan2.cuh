@@ -608,8 +608,8 @@ __global__ void __launch_bounds__(256) k_scan_step(ScanArgs a) {
     for (int k = 0; k < kStepPPW; ++k) hv[k] = __ldcs(st + (warp + 8 * k) * 32 + lane);
   }
   // Under programmatic dependent launch the state loads above overlap the
-  // previous kernel's drain.  They may: of the kernels that write a state,
-  // this one and k_scan_seq issue no early trigger, and k_ssd_pass is always
+  // previous kernel's drain.  They may: of the kernels that write a state, this
+  // one, k_scan_seq and k_reorder_rows issue no early trigger, and k_ssd_pass is always
   // followed by k_ssd_out, which triggers only after waiting for it -- so every
   // kernel launched after a state's writer starts once that state is written.
   // Everything below reads the conv's and in_proj's outputs.

@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(128) k_embed_rows(const int32_t *__restrict__ 
 // writes any, so no second buffer and no order between threads is needed.
 // In place, a beam that keeps its own state is neither read nor written.  A
 // parent outside the source's beams leaves the row as it was and sets the
-// device error word.
+// device error word.  Like every kernel that writes a carried state it issues no
+// early trigger: k_scan_step loads its state before its dependency wait.
 // Bound by memory: 64 layers of 4 x 8 beams, 5.4 GB of int32 states, 1.2 ms, 6.6
 // TB/s of what has to move.
 constexpr int kReorderBufs = 128;  // buffers per launch
@@ -378,7 +379,6 @@ template <typename U, int G>
 __global__ void __launch_bounds__(kReorderThreads)
     k_reorder_rows(const __grid_constant__ ReorderArgs a) {
   pdl_wait();
-  pdl_trigger();
   int lo = 0, hi = a.n;  // the buffer of this block
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;

@@ -41,3 +41,12 @@ def test_every_kernel_launched_early_waits():
     names = launched()
     assert len(names) >= 20 and "k_fp8_gemm_tc" in names
     assert [n for n in names if "pdl_wait()" not in body(n)] == []
+
+
+def test_kernels_that_write_a_state_do_not_trigger():
+    """k_scan_step loads its state before its wait, so whatever is launched behind
+    a kernel that writes states must start after that kernel's end."""
+    step = body("k_scan_step")
+    assert step.index("a.state + headrow") < step.index("pdl_wait()")
+    for name in ("k_scan_step", "k_scan_seq", "k_reorder_rows"):
+        assert "pdl_trigger" not in body(name), name
