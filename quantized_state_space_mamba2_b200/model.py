@@ -6,6 +6,8 @@ through the ctypes binding in `lib`.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -15,6 +17,12 @@ from .synth import MixerShape
 
 def _dev(a, dtype, device):
     return torch.from_numpy(np.ascontiguousarray(a)).to(device=device, dtype=dtype).contiguous()
+
+
+def _on(stream):
+    """Tensors made under it belong to `stream` (default: the current one): the
+    allocator hands their memory out again only behind that stream's work."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 class DeviceLayer:
@@ -191,6 +199,8 @@ class DeviceStack:
 class DeviceLM:
     """Token ids in, next tokens out: an embedding table, a DeviceStack, the final
     RMSNorm and an output head, with beam search over the stack's carried states.
+    What a call with stream= makes and returns belongs to that stream, as if it
+    were the current one; the tensors passed in must be ready there.
 
     embedding [V, d_model] (fp32) is held as e4m3 codes with a scale per
     128 x 128 block; head [V, d_model] likewise, or None where the output head
@@ -220,8 +230,9 @@ class DeviceLM:
     def embed(self, ids: torch.Tensor, out=None, stream=None) -> torch.Tensor:
         """Rows [*ids.shape, d_model] of int32 token ids (-1: zeros)."""
         d = self.shape.d_model
-        out = torch.empty(*ids.shape, d, device=self.device) if out is None else out
-        lib.embed_rows(ids, self.table, out.view(-1, d), self.table_s, self.embed_scale, stream)
+        with _on(stream):
+            out = torch.empty(*ids.shape, d, device=self.device) if out is None else out
+            lib.embed_rows(ids, self.table, out.view(-1, d), self.table_s, self.embed_scale)
         return out
 
     def calibrate(self, ids: torch.Tensor):
@@ -239,38 +250,40 @@ class DeviceLM:
 
     def logits(self, h: torch.Tensor, residual=None, bufs=None, stream=None) -> torch.Tensor:
         """Logits [rows, V] (fp32) of the rows h (+ residual), [rows, d_model]."""
-        q, s, y = self.head_buffers(h.shape[0]) if bufs is None else bufs
-        lib.add_norm_quant(h, self.norm_w, q, s, residual=residual, stream=stream)
-        lib.fp8_gemm(q, s, self.head, self.head_s, y, stream)
+        with _on(stream):
+            q, s, y = self.head_buffers(h.shape[0]) if bufs is None else bufs
+            lib.add_norm_quant(h, self.norm_w, q, s, residual=residual)
+            lib.fp8_gemm(q, s, self.head, self.head_s, y)
         return y
 
     def prefill(self, ids: torch.Tensor, states=None, stream=None) -> torch.Tensor:
         """Logits [B, V] of the token after ids [B, T]; states are carried."""
-        x = self.embed(ids, stream=stream)
-        B, T, _ = x.shape
-        ws = self.stack.layers[0].workspace(B, T)
-        h = torch.empty_like(x)
-        last = len(self.stack.layers) - 1
-        for i, L in enumerate(self.stack.layers):
-            cs, ss = states[i] if states is not None else (None, None)
-            # the last layer's residual addition is the norm's
-            L.prefill(x, residual=i < last, conv_state=cs, ssm_state=ss,
-                      out=x if i < last else h, ws=ws, stream=stream)
-        return self.logits(h[:, -1], residual=x[:, -1], stream=stream)
+        with _on(stream):
+            x = self.embed(ids)
+            B, T, _ = x.shape
+            ws = self.stack.layers[0].workspace(B, T)
+            h = torch.empty_like(x)
+            last = len(self.stack.layers) - 1
+            for i, L in enumerate(self.stack.layers):
+                cs, ss = states[i] if states is not None else (None, None)
+                # the last layer's residual addition is the norm's
+                L.prefill(x, residual=i < last, conv_state=cs, ssm_state=ss,
+                          out=x if i < last else h, ws=ws)
+            return self.logits(h[:, -1], residual=x[:, -1])
 
     def decode(self, ids: torch.Tensor, states: list, x=None, h=None, ws=None, bufs=None,
                stream=None) -> torch.Tensor:
         """Logits [rows, V] after one more token ids [rows]; states are updated.
         x, h [rows, d_model], ws and bufs (head_buffers) may be kept by the caller."""
         rows = ids.numel()
-        x = self.embed(ids, out=x, stream=stream)
-        h = torch.empty_like(x) if h is None else h
-        ws = self.stack.layers[0].workspace(rows, 1) if ws is None else ws
-        last = len(self.stack.layers) - 1
-        for i, L in enumerate(self.stack.layers):
-            L.decode(x, *states[i], residual=i < last, out=x if i < last else h, ws=ws,
-                     stream=stream)
-        return self.logits(h, residual=x, bufs=bufs, stream=stream)
+        with _on(stream):
+            x = self.embed(ids, out=x)
+            h = torch.empty_like(x) if h is None else h
+            ws = self.stack.layers[0].workspace(rows, 1) if ws is None else ws
+            last = len(self.stack.layers) - 1
+            for i, L in enumerate(self.stack.layers):
+                L.decode(x, *states[i], residual=i < last, out=x if i < last else h, ws=ws)
+            return self.logits(h, residual=x, bufs=bufs)
 
     def beam_search(self, ids: torch.Tensor, beams: int, steps: int, eos: int = -1):
         """`steps` tokens after ids [B, T] (int32): tokens [B, beams, steps] (int32)

@@ -192,3 +192,66 @@ def test_plain_beam_is_a_sort_of_all_candidates():
     v, i = torch.sort(c.view(3, -1), dim=1, descending=True, stable=True)
     assert torch.allclose(out, v[:, :7], rtol=0, atol=1e-12)
     assert torch.equal(par * 50 + tok, i[:, :7])
+
+
+def test_a_model_on_a_side_stream_owns_its_buffers(monkeypatch):
+    """stream= of DeviceLM: what a call allocates comes from that stream's memory
+    and every step runs there (stand-ins for the kernels and the streams)."""
+    import contextlib
+
+    from quantized_state_space_mamba2_b200 import lib, model
+    from quantized_state_space_mamba2_b200.synth import MixerShape
+    now, made, ran = [None], [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        old, now[0] = now[0], s if s is not None else now[0]
+        yield
+        now[0] = old
+
+    def recorded(make):
+        def f(*a, **kw):
+            made.append(now[0])
+            return make(*a, **kw)
+        return f
+
+    def step(name):
+        def f(*a, stream=None, **kw):
+            ran.append((name, now[0] if stream is None else stream))
+        return f
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for name in ("empty", "empty_like", "zeros"):
+        monkeypatch.setattr(torch, name, recorded(getattr(torch, name)))
+    monkeypatch.setattr(lib, "add_norm_quant", step("norm"))
+    monkeypatch.setattr(lib, "fp8_gemm", lambda *a: step("product")(stream=a[5] if len(a) > 5 else None))
+    monkeypatch.setattr(lib, "embed_rows",
+                        lambda *a: step("embed")(stream=a[5] if len(a) > 5 else None))
+    shape = MixerShape(d_model=256, d_inner=512, headdim=64, d_state=128)
+
+    class Layer:
+        def workspace(self, B, T):
+            return torch.empty(8)
+
+        def prefill(self, x, stream=None, **kw):
+            step("layer")(stream=stream)
+
+        decode = lambda self, x, *states, stream=None, **kw: step("layer")(stream=stream)
+
+    lm = object.__new__(model.DeviceLM)
+    lm.shape, lm.embed_scale, lm.device = shape, 1.0, torch.device("cpu")
+    lm.stack = type("Stack", (), {"layers": [Layer(), Layer()]})()
+    lm.table, lm.table_s = lm.head, lm.head_s = torch.zeros(301, 256), torch.zeros(3, 2)
+    lm.norm_w = torch.ones(256)
+    ids, h = torch.zeros(2, 5, dtype=torch.int32), torch.zeros(2, 256)
+    calls = [lambda s: lm.embed(ids, stream=s), lambda s: lm.logits(h, stream=s),
+             lambda s: lm.prefill(ids, stream=s),
+             lambda s: lm.decode(ids[:, 0], [(None, None)] * 2, stream=s)]
+    for want in ("side", None):
+        for call in calls:
+            made.clear()
+            ran.clear()
+            call(want)
+            assert made and set(made) == {want}
+            assert ran and {s for _, s in ran} == {want}
+            assert now[0] is None
