@@ -26,10 +26,16 @@ def _on(stream):
 
 
 class DeviceLayer:
-    """One prepared mixer layer: quantised weights + exponent table on the GPU."""
+    """One prepared mixer layer: quantised weights + exponent table on the GPU.
+    What a call with stream= allocates belongs to that stream, as if it were the
+    current one."""
 
     def __init__(self, params: dict, shape: MixerShape, rotate: int = 1, mode: int = lib.FM_DYNAMIC,
                  prenorm: bool = False, device="cuda", stream=None):
+        with _on(stream):
+            self._prepare(params, shape, rotate, mode, prenorm, device)
+
+    def _prepare(self, params, shape, rotate, mode, prenorm, device):
         s = shape
         self.shape, self.rotate, self.mode, self.prenorm = s, rotate, mode, prenorm
         self.device = torch.device(device)
@@ -39,8 +45,8 @@ class DeviceLayer:
         self.w_in_s = torch.empty(s.n_in, dtype=torch.float32, device=self.device)
         self.w_out_q = torch.empty((s.d_model, s.d_inner), dtype=torch.int8, device=self.device)
         self.w_out_s = torch.empty(s.d_model, dtype=torch.float32, device=self.device)
-        lib.prepare_linear(w_in, rotate, self.w_in_q, self.w_in_s, stream)
-        lib.prepare_linear(w_out, rotate, self.w_out_q, self.w_out_s, stream)
+        lib.prepare_linear(w_in, rotate, self.w_in_q, self.w_in_s)
+        lib.prepare_linear(w_out, rotate, self.w_out_q, self.w_out_s)
         self.conv_w = f32(params["conv_w"])
         self.conv_b = f32(params["conv_b"])
         self.a_log = f32(params["a_log"])
@@ -56,7 +62,7 @@ class DeviceLayer:
         self.D_q = torch.empty(s.nheads, dtype=torch.int32, device=self.device)
         self.static_amax = torch.zeros(4, dtype=torch.float32, device=self.device)
         lib.prepare_mixer_params(s, self.conv_w, self.a_log, self.D, self.conv_wq, self.A_q,
-                                 self.D_q, self.exps, stream)
+                                 self.D_q, self.exps)
         del w_in, w_out
         self.struct = self._make_struct()
         p = lambda t: t.data_ptr()
@@ -74,11 +80,12 @@ class DeviceLayer:
     def calibrate(self, xcal: torch.Tensor, residual: bool = False, stream=None) -> torch.Tensor:
         """Calibrate on xcal [B, T, d_model] (fp32, device); returns the layer output."""
         B, T, _ = xcal.shape
-        ws = torch.empty(lib.calib_workspace_bytes(self.shape, B, T), dtype=torch.uint8,
-                         device=self.device)
-        out = torch.empty_like(xcal)
-        lib.calibrate_layer(self.struct, self.conv_b, self.exps, self.conv_bq, self.static_amax,
-                            xcal, B, T, int(residual), out, ws, stream)
+        with _on(stream):
+            ws = torch.empty(lib.calib_workspace_bytes(self.shape, B, T), dtype=torch.uint8,
+                             device=self.device)
+            out = torch.empty_like(xcal)
+            lib.calibrate_layer(self.struct, self.conv_b, self.exps, self.conv_bq, self.static_amax,
+                                xcal, B, T, int(residual), out, ws)
         return out
 
     def exponents(self) -> dict:
@@ -101,18 +108,19 @@ class DeviceLayer:
     def prefill(self, x: torch.Tensor, residual: bool = False, conv_state=None, ssm_state=None,
                 out=None, ws=None, stream=None) -> torch.Tensor:
         B, T, _ = x.shape
-        out = torch.empty_like(x) if out is None else out
-        ws = self.workspace(B, T) if ws is None else ws
-        lib.mixer_prefill(self.struct, x, B, T, int(residual), conv_state, ssm_state, out, ws,
-                          stream)
+        with _on(stream):
+            out = torch.empty_like(x) if out is None else out
+            ws = self.workspace(B, T) if ws is None else ws
+            lib.mixer_prefill(self.struct, x, B, T, int(residual), conv_state, ssm_state, out, ws)
         return out
 
     def decode(self, x: torch.Tensor, conv_state, ssm_state, residual: bool = False, out=None,
                ws=None, stream=None) -> torch.Tensor:
         B = x.shape[0]
-        out = torch.empty_like(x) if out is None else out
-        ws = self.workspace(B, 1) if ws is None else ws
-        lib.decode_step(self.struct, x, B, int(residual), conv_state, ssm_state, out, ws, stream)
+        with _on(stream):
+            out = torch.empty_like(x) if out is None else out
+            ws = self.workspace(B, 1) if ws is None else ws
+            lib.decode_step(self.struct, x, B, int(residual), conv_state, ssm_state, out, ws)
         return out
 
     # ------------------------------------------------------------ FastMamba-LQ
@@ -125,10 +133,11 @@ class DeviceLayer:
         """The LQ variant of this layer: the same W8A8 linears and scales, the
         conv, scan and gate in fp32 (fp32 states from lq_new_states)."""
         B, T, _ = x.shape
-        out = torch.empty_like(x) if out is None else out
-        ws = self.lq_workspace(B, T) if ws is None else ws
-        lib.lq_mixer_prefill(self.struct, self.lq_struct, x, B, T, int(residual), conv_state,
-                             ssm_state, out, ws, stream)
+        with _on(stream):
+            out = torch.empty_like(x) if out is None else out
+            ws = self.lq_workspace(B, T) if ws is None else ws
+            lib.lq_mixer_prefill(self.struct, self.lq_struct, x, B, T, int(residual), conv_state,
+                                 ssm_state, out, ws)
         return out
 
     def lq_new_states(self, B: int):
@@ -164,10 +173,11 @@ class DeviceStack:
     def prefill_(self, r: torch.Tensor, ws=None, states=None, stream=None) -> torch.Tensor:
         """In place: r <- r + mixer_l(RMSNorm(r)) for every layer."""
         B, T, _ = r.shape
-        ws = self.layers[0].workspace(B, T) if ws is None else ws
-        for i, L in enumerate(self.layers):
-            cs, ss = states[i] if states is not None else (None, None)
-            L.prefill(r, residual=True, conv_state=cs, ssm_state=ss, out=r, ws=ws, stream=stream)
+        with _on(stream):
+            ws = self.layers[0].workspace(B, T) if ws is None else ws
+            for i, L in enumerate(self.layers):
+                cs, ss = states[i] if states is not None else (None, None)
+                L.prefill(r, residual=True, conv_state=cs, ssm_state=ss, out=r, ws=ws)
         return r
 
     def stack_workspace(self, B: int, T: int, n_chunks: int) -> torch.Tensor:
@@ -180,8 +190,9 @@ class DeviceStack:
         sequence is cut into runs that pipeline through the layers on the
         library's own streams (bit-identical to prefill_)."""
         B, T, _ = r.shape
-        ws = self.stack_workspace(B, T, n_chunks) if ws is None else ws
-        lib.stack_prefill([L.struct for L in self.layers], r, B, T, states, n_chunks, ws, stream)
+        with _on(stream):
+            ws = self.stack_workspace(B, T, n_chunks) if ws is None else ws
+            lib.stack_prefill([L.struct for L in self.layers], r, B, T, states, n_chunks, ws)
         return r
 
     def prefill_host(self, x_host: torch.Tensor, out_host: torch.Tensor, x_dev: torch.Tensor,
@@ -190,9 +201,10 @@ class DeviceStack:
         out_host out (pinned host tensors), x_dev the device rows it runs in.
         Asynchronous on the stream: out_host is final after synchronising it."""
         B, T, _ = x_host.shape
-        ws = self.stack_workspace(B, T, n_chunks) if ws is None else ws
-        lib.stack_prefill_host([L.struct for L in self.layers], x_host, out_host, x_dev, B, T,
-                               states, n_chunks, ws, stream)
+        with _on(stream):
+            ws = self.stack_workspace(B, T, n_chunks) if ws is None else ws
+            lib.stack_prefill_host([L.struct for L in self.layers], x_host, out_host, x_dev, B, T,
+                                   states, n_chunks, ws)
         return out_host
 
 

@@ -58,3 +58,51 @@ def test_a_model_on_a_side_stream(lib):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(torch.equal(a, b) for p, q in zip(states2, states) for a, b in zip(p, q))
     lib.sync_status()
+
+
+def test_layers_on_a_side_stream(lib):
+    """A layer and a stack prepared, calibrated and run on a busy side stream."""
+    from quantized_state_space_mamba2_b200.model import DeviceLayer, DeviceStack
+    shape = S.MixerShape(d_model=256, d_inner=512, headdim=64, d_state=128)
+    params = [S.layer_params(shape, 90 + l) for l in range(2)]
+    x = torch.from_numpy(S.activations(2, 40, 256, seed=3, n_outliers=4, outlier_scale=20.0,
+                                       outlier_seed=4)).cuda()
+    host, first = x.cpu().pin_memory(), x[:, 0].contiguous()
+
+    def run(stream, between):
+        out = []
+
+        def keep(t):
+            between()
+            out.append(t)
+
+        L = DeviceLayer(params[0], shape, prenorm=True, stream=stream)
+        keep(L.calibrate(x, stream=stream))
+        keep(L.prefill(x, stream=stream))
+        states = L.new_states(2)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                busy.add_(1.0)
+        keep(L.decode(first, *states, stream=stream))
+        keep(L.lq_prefill(x, stream=stream))
+        stack = DeviceStack(params, shape)
+        stack.calibrate(x)
+        rows = [x.clone() for _ in range(3)]
+        back = torch.empty_like(host).pin_memory()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                busy.add_(1.0)
+        keep(stack.prefill_(rows[0], stream=stream))
+        keep(stack.prefill_pipelined_(rows[1], 2, stream=stream))
+        keep(stack.prefill_host(host, back, rows[2], 2, stream=stream))
+        torch.cuda.synchronize()
+        return [t.cuda() for t in out] + list(states)
+
+    busy = torch.zeros(1 << 26, device="cuda")
+    want = run(None, lambda: None)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(side, overwrite), want))
+    lib.sync_status()

@@ -255,3 +255,47 @@ def test_a_model_on_a_side_stream_owns_its_buffers(monkeypatch):
             assert made and set(made) == {want}
             assert ran and {s for _, s in ran} == {want}
             assert now[0] is None
+
+
+def test_a_layer_on_a_side_stream_owns_its_buffers(monkeypatch):
+    """stream= of DeviceLayer and DeviceStack, with the same stand-ins."""
+    import contextlib
+
+    from quantized_state_space_mamba2_b200 import lib, model
+    now, made, ran = [None], [], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        old, now[0] = now[0], s
+        yield
+        now[0] = old
+
+    def recorded(make):
+        def f(*a, **kw):
+            made.append(now[0])
+            return make(*a, **kw)
+        return f
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for name in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, name, recorded(getattr(torch, name)))
+    for name in ("calib_workspace_bytes", "workspace_bytes", "lq_workspace_bytes", "stack_workspace_bytes"):
+        monkeypatch.setattr(lib, name, lambda *a: 16)
+    for name, last in (("calibrate_layer", 11), ("mixer_prefill", 9), ("decode_step", 8),
+                       ("lq_mixer_prefill", 10), ("stack_prefill", 7), ("stack_prefill_host", 9)):
+        monkeypatch.setattr(lib, name, lambda *a, last=last: ran.append(a[last] if len(a) > last else now[0]))
+    L = object.__new__(model.DeviceLayer)
+    L.__dict__.update(dict.fromkeys(("shape", "struct", "lq_struct", "conv_b", "exps", "conv_bq",
+                                     "static_amax")), device=torch.device("cpu"))
+    stack = object.__new__(model.DeviceStack)
+    stack.shape, stack.layers = None, [L, L]
+    x = torch.zeros(2, 5, 32)
+    for call in (lambda: L.calibrate(x, stream="side"), lambda: L.prefill(x, stream="side"),
+                 lambda: L.decode(x[:, 0], None, None, stream="side"), lambda: L.lq_prefill(x, stream="side"),
+                 lambda: stack.prefill_(x, stream="side"), lambda: stack.prefill_pipelined_(x, stream="side"),
+                 lambda: stack.prefill_host(x, x, x, stream="side")):
+        made.clear()
+        ran.clear()
+        call()
+        assert made and set(made) == {"side"} and ran and set(ran) == {"side"}
+        assert now[0] is None
