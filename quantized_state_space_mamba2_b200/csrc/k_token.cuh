@@ -70,15 +70,12 @@ __device__ __forceinline__ float group8_max(float v) {
   return v;
 }
 
-// v = r w c in 64 bits, rounded to fp32 towards zero with the lost bits kept as
-// a last 1: a later rounding to fewer than 22 bits is then that of v itself
+// v rounded to fp32 towards zero with the lost bits kept as a last 1: a later
+// rounding to fewer than 22 bits is then that of v itself
 __device__ __forceinline__ float sticky(double v) {
   float f = __double2float_rz(v);
   if ((double)f != v) f = __uint_as_float(__float_as_uint(f) | 1u);
   return f;
-}
-__device__ __forceinline__ float sticky_product(float r, float w, double c) {
-  return sticky(__dmul_rn(__dmul_rn((double)r, (double)w), c));
 }
 
 // Whether t, within 4 ulp of y / s, may round to another code than it does:
@@ -290,13 +287,15 @@ __global__ void __launch_bounds__(256) k_prepare_linear_fp8(const float *__restr
   a = warp_max(lane < 8 ? s_red[lane] : 0.0f);
   if (a < kNormTiny) a = 0.0f;
   const float s = (float)__ddiv_rn((double)a, 448.0);
-  const double c = s > 0.0f ? __drcp_rn((double)s) : 0.0;
+  // A quotient in 64 bits is on the tie's side that W / s is on: a tie has 5 bits
+  // and s 24, so W / s is a tie exactly, or off by more than 2^-30 of it.  (A
+  // product with 1 / s can miss an exact tie.)
+  auto arg = [s](float v) { return s > 0.0f ? sticky(__ddiv_rn((double)v, (double)s)) : 0.0f; };
   for (int i = warp; i < 128; i += 8)
     if (n0 + i < N && k < K) {
       const float4 v = load4(W + (n0 + i) * K + k);
-      const float t0 = sticky_product(v.x, 1.0f, c), t1 = sticky_product(v.y, 1.0f, c);
-      const float t2 = sticky_product(v.z, 1.0f, c), t3 = sticky_product(v.w, 1.0f, c);
-      *reinterpret_cast<uint32_t *>(Wq + (n0 + i) * K + k) = e4m3x2(t0, t1) | (e4m3x2(t2, t3) << 16);
+      *reinterpret_cast<uint32_t *>(Wq + (n0 + i) * K + k) =
+          e4m3x2(arg(v.x), arg(v.y)) | (e4m3x2(arg(v.z), arg(v.w)) << 16);
     }
   if (threadIdx.x == 0) s_w[(long long)blockIdx.y * gridDim.x + blockIdx.x] = s;
 }

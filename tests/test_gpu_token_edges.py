@@ -65,3 +65,26 @@ def test_norm_on_exact_ties(lib, kind, dtype):
     assert bool((scales == (2.0 ** -7 if kind == "e4m3" else 2.0 ** -5)).all())
     assert int((sure == 0).sum()) >= 4 * len(ties)
     assert torch.equal(s, scales) and torch.equal(q.float().to(F64), codes)
+
+
+# ------------------------------------------------------------------ prepared weights
+SCALES = [1, 3, 49, 75, 77, 91, 93, 99, 103, 147, 555, 599]
+
+
+def test_prepared_weights_on_exact_ties(lib):
+    """Blocks whose scale is a small integer: W / s is exactly in the middle between
+    two codes, which goes to the even one."""
+    W = torch.zeros(128, 128 * len(SCALES), dtype=F64)
+    t = torch.tensor([k / 16 * 2.0 ** e for k in range(17, 32, 2) for e in (-6, -5, 0, 7)]
+                     + [k / 1024 for k in range(1, 16, 2)], dtype=F64)
+    for i, j in enumerate(SCALES):
+        W[0, 128 * i] = 448 * j
+        W[1, 128 * i:128 * i + len(t)] = j * t
+        W[2, 128 * i:128 * i + len(t)] = -j * t
+    assert torch.equal(W.float().to(F64), W)
+    q, s = torch.zeros(W.shape, device="cuda").to(E4M3), torch.zeros(1, len(SCALES), device="cuda")
+    lib.prepare_linear_fp8(W.float().cuda(), q, s)
+    lib.sync_status()
+    assert s[0].tolist() == SCALES
+    want = P.e4m3_round(W / s.cpu().to(F64).repeat_interleave(128, 1))
+    assert torch.equal(q.float().cpu().to(F64), want)
