@@ -271,17 +271,15 @@ __global__ void __launch_bounds__(256) k_prepare_linear_fp8(const float *__restr
   const long long n0 = (long long)blockIdx.y * 128;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = k0 + 4 * lane;
-  float a = 0.0f;
-  bool finite = true;
+  uint32_t a_bits = 0;  // of the largest |W|: ordered as the values, NaN above all
   for (int i = warp; i < 128; i += 8)
     if (n0 + i < N && k < K) {
       const float4 v = load4(W + (n0 + i) * K + k);
-      const float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-      finite = finite && fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) <= 3.402823466e38f;
-      a = fmaxf(a, m);
+      a_bits = max(a_bits, max(max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu),
+                               max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu)));
     }
-  if (!finite) raise_error(kErrNonfinite);
-  a = warp_max(a);
+  if (a_bits >= 0x7F800000u) raise_error(kErrNonfinite);
+  float a = warp_max(__uint_as_float(a_bits));
   if (lane == 0) s_red[warp] = a;
   __syncthreads();
   a = warp_max(lane < 8 ? s_red[lane] : 0.0f);

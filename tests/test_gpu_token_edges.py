@@ -1,5 +1,5 @@
 """The token loop's operators at the borders of their definitions: exact ties of
-codes."""
+codes, the largest weights."""
 import math
 
 import pytest
@@ -88,3 +88,25 @@ def test_prepared_weights_on_exact_ties(lib):
     assert s[0].tolist() == SCALES
     want = P.e4m3_round(W / s.cpu().to(F64).repeat_interleave(128, 1))
     assert torch.equal(q.float().cpu().to(F64), want)
+
+
+def test_prepared_weights_of_the_largest_magnitudes(lib):
+    """Finite weights are no error however large; a NaN or an infinity is one."""
+    top = torch.finfo(torch.float32).max
+    W = torch.full((256, 144), 1e38, device="cuda")
+    W[3, 5], W[130, 7], W[255, 143] = top, -top, top
+    q, s = torch.zeros(W.shape, device="cuda").to(E4M3), torch.zeros(2, 2, device="cuda")
+    lib.prepare_linear_fp8(W, q, s)
+    lib.sync_status()
+    want_s = torch.tensor([[top, 1e38], [top, top]], device="cuda").to(F64) / 448.0
+    assert torch.equal(s, want_s.float())
+    v = W.to(F64) / s.to(F64).repeat_interleave(128, 0).repeat_interleave(128, 1)[:, :144]
+    assert torch.equal(q.float().to(F64), P.e4m3_round(v))
+    for bad in (math.nan, math.inf, -math.inf):
+        for at in ((0, 0), (255, 143), (7, 130)):
+            V = W.clone()
+            V[at] = bad
+            lib.prepare_linear_fp8(V, q, s)
+            with pytest.raises(lib.FmError) as e:
+                lib.sync_status()
+            assert e.value.status == 5
