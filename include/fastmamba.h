@@ -667,6 +667,10 @@ fm_status fm_embed_rows(const int32_t *ids, int64_t M, const void *table, fm_dty
  * the lowest k V + v: out_scores [B, n_out] = fl32(c) (at least the lowest
  * fp32 value), parent (the beam k) and token (v) [B, n_out].  Candidates of one
  * beam are ordered by their logits, those of different beams by c in 64 bits.
+ * The log sum of a beam is formed from fp32 exponentials, off by at most (2.25
+ * ln V + 20) 2^-24, which is in its scores; where candidates of different beams
+ * lie closer than that tells apart, the beams' log sums are formed again in 64
+ * bits (which takes longer: such rows are read twice).
  *   - A logit of -inf is no candidate, nor is any of a beam whose score is
  *     -inf or NaN; a NaN logit counts as -inf, +inf as the largest fp32 value.
  *   - finished [B, beams] or NULL: a beam with a nonzero flag has the one

@@ -246,9 +246,24 @@ extern "C" fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t l
   };
   FM_TRY(type == FM_F32 ? go(float()) : go(__nv_bfloat16()));
   FM_TRY(launched("k_beam_chunks"));
-  FM_TRY(launch_ex("k_beam_merge", k_beam_merge, (unsigned)B, 32 * beams, 0, st,
-                   (const unsigned long long *)keys, (const float *)tops, (const double *)sums, S,
-                   beams, scores, finished, eos, n_out, out_scores, parent, token, out_finished));
+  // How far a log sum of k_beam_chunks may be off.  With d = top - l, the argument
+  // of an exponential is d log2(e) with three relative errors (the difference, the
+  // constant, the product: 2^-24 + 2^-26 + 2^-24), the exponential has 2^-22, and
+  // up to 16 of them are added in fp32 (15 roundings), the rest in 64 bits.  The
+  // mean of d under the softmax is its entropy less the log sum, so at most ln V.
+  const double tol = (2.25 * std::log((double)V) + 20.0) * 0x1p-24;
+  // an SM holds 32 warps of the merge: as many each as lets its entries run side by
+  // side (one beam has no other to be close to)
+  const int per_sm = (B + sm_count() - 1) / sm_count();
+  const int warps = beams == 1 ? 1 : std::max(beams, 32 / per_sm);
+  auto merge = [&](auto t) -> fm_status {
+    using T = decltype(t);
+    return launch_ex("k_beam_merge", k_beam_merge<T>, (unsigned)B, 32 * warps, 0, st, (const unsigned long long *)keys,
+                     (const float *)tops, (const double *)sums, S, beams, (const T *)logits,
+                     (long long)ld, (unsigned)V, tol, scores, finished, eos, n_out, out_scores, parent,
+                     token, out_finished);
+  };
+  FM_TRY(type == FM_F32 ? merge(float()) : merge(__nv_bfloat16()));
   return launched("k_beam_merge");
 }
 

@@ -259,117 +259,196 @@ __device__ __forceinline__ unsigned long long warp_max_key(unsigned long long k)
   return k;
 }
 
+// sum_v exp(l[v] - top) of a row in 64 bits, by the whole CTA (its result in
+// thread 0): which thread adds an element depends on its index alone.
+template <typename T>
+__device__ __forceinline__ double beam_exact_sum(const T *__restrict__ row, unsigned V,
+                                                 double top, double *s_part) {
+  double t = 0.0;
+#pragma unroll 1  // four at once need more registers than 32 warps have
+  for (unsigned i = threadIdx.x; i < V; i += blockDim.x)
+    t += exp((double)beam_logit((float)row[i]) - top);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  __syncthreads();  // s_part's last values have been read
+  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = t;
+  __syncthreads();
+  t = 0.0;
+  if (threadIdx.x == 0)
+    for (unsigned i = 0; i < blockDim.x / 32; ++i) t += s_part[i];
+  return t;
+}
+
 // One CTA per batch entry, one warp per beam for its log sum and its n largest
 // logits (the largest key below the last one, n times over its chunks' lists),
 // then one warp, lane k at the head of beam k's list.
+//
+// The chunks' log sums are off by up to tol each, so the order of two beams'
+// candidates that lie within it is not known yet: the log sums of such beams are
+// then formed again, in 64 bits from the logits, and the lists merged once more.
+// Compared are neighbours in the merged order of different beams (gaps that each
+// exceed both beams' errors add up to more than those of the two ends), and the
+// last one taken with the head of each list.  Random logits call for it in some
+// 10^-4 of the entries; rows that are equal, with equal scores, always (64 x 8 x
+// 100003 bf16: 509 us then, 53.8 us on random logits; 1760 us with 8 warps per
+// CTA).  More warps than beams are there for that work alone.
+
+template <typename T>
 __global__ void __launch_bounds__(32 * kBeamMax)
     k_beam_merge(const unsigned long long *__restrict__ keys, const float *__restrict__ tops,
-                 const double *__restrict__ sums, int S, int beams, const float *scores,
-                 const uint8_t *finished, int eos, int n_out, float *out_scores, int32_t *parent,
-                 int32_t *token, uint8_t *out_finished) {
+                 const double *__restrict__ sums, int S, int beams, const T *__restrict__ logits,
+                 long long ld, unsigned V, double tol, const float *scores, const uint8_t *finished,
+                 int eos, int n_out, float *out_scores, int32_t *parent, int32_t *token,
+                 uint8_t *out_finished) {
   pdl_wait();
   pdl_trigger();
   __shared__ unsigned long long s_list[kBeamMax][kBeamMax];
-  __shared__ double s_lse[kBeamMax];
-  __shared__ float s_score[kBeamMax];
+  __shared__ double s_lse[kBeamMax], s_part[kBeamMax];
+  __shared__ float s_score[kBeamMax], s_top[kBeamMax];
   __shared__ uint8_t s_done[kBeamMax];
+  __shared__ unsigned s_redo;
   const int lane = threadIdx.x & 31, beam = threadIdx.x >> 5;
-  const long long row = (long long)blockIdx.x * beams + beam;
-  // every first load on its way at once (what a row that was not read left in
-  // the workspace is loaded too, and not used)
-  const float score = scores[row];
-  const uint8_t flag = finished ? finished[row] : 0;
-  const float *tp = tops + row * S;
-  const double *sp = sums + row * S;
-  const unsigned long long *kp = keys + row * S * n_out;
-  const int all = S * n_out;
-  constexpr int kHold = 8;  // keys per lane held in registers
-  unsigned long long own[kHold], last = ~0ull;
+  if (beam < beams) {
+    const long long row = (long long)blockIdx.x * beams + beam;
+    // every first load on its way at once (what a row that was not read left in
+    // the workspace is loaded too, and not used)
+    const float score = scores[row];
+    const uint8_t flag = finished ? finished[row] : 0;
+    const float *tp = tops + row * S;
+    const double *sp = sums + row * S;
+    const unsigned long long *kp = keys + row * S * n_out;
+    const int all = S * n_out;
+    constexpr int kHold = 8;  // keys per lane held in registers
+    unsigned long long own[kHold], last = ~0ull;
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) own[i] = 32 * i + lane < all ? kp[32 * i + lane] : 0;
-  const float top = lane < S ? tp[lane] : -INFINITY;
-  const double sum = lane < S ? sp[lane] : 0.0;
-  const bool finish = flag != 0, dead = !(score > -INFINITY);
-  if (lane == 0) {
-    s_score[beam] = score;
-    s_done[beam] = finish;
-  }
-  if (!finish && !dead) {
-    float m = top;
-    for (int i = 32 + lane; i < S; i += 32) m = fmaxf(m, tp[i]);
-    m = warp_max(m);
-    double t = sum > 0.0 ? sum * exp((double)top - (double)m) : 0.0;
-    for (int i = 32 + lane; i < S; i += 32)
-      if (sp[i] > 0.0) t += sp[i] * exp((double)tp[i] - (double)m);
+    for (int i = 0; i < kHold; ++i) own[i] = 32 * i + lane < all ? kp[32 * i + lane] : 0;
+    const float top = lane < S ? tp[lane] : -INFINITY;
+    const double sum = lane < S ? sp[lane] : 0.0;
+    const bool finish = flag != 0, dead = !(score > -INFINITY);
+    if (lane == 0) {
+      s_score[beam] = score;
+      s_done[beam] = finish;
+    }
+    if (!finish && !dead) {
+      float m = top;
+      for (int i = 32 + lane; i < S; i += 32) m = fmaxf(m, tp[i]);
+      m = warp_max(m);
+      double t = sum > 0.0 ? sum * exp((double)top - (double)m) : 0.0;
+      for (int i = 32 + lane; i < S; i += 32)
+        if (sp[i] > 0.0) t += sp[i] * exp((double)tp[i] - (double)m);
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) s_lse[beam] = (double)m + log(t);
-    for (int n = 0; n < n_out; ++n) {
-      unsigned long long best = 0;
+      for (int o = 16; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane == 0) {
+        s_lse[beam] = (double)m + log(t);
+        s_top[beam] = m;
+      }
+      for (int n = 0; n < n_out; ++n) {
+        unsigned long long best = 0;
 #pragma unroll
-      for (int i = 0; i < kHold; ++i)
-        if (own[i] < last && own[i] > best) best = own[i];
-      for (int i = 32 * kHold + lane; i < all; i += 32)
-        if (kp[i] < last && kp[i] > best) best = kp[i];
-      last = warp_max_key(best);
-      if (lane == 0) s_list[beam][n] = last;
-      if (last == 0) {
-        for (int j = n + 1 + lane; j < n_out; j += 32) s_list[beam][j] = 0;
-        break;
+        for (int i = 0; i < kHold; ++i)
+          if (own[i] < last && own[i] > best) best = own[i];
+        for (int i = 32 * kHold + lane; i < all; i += 32)
+          if (kp[i] < last && kp[i] > best) best = kp[i];
+        last = warp_max_key(best);
+        if (lane == 0) s_list[beam][n] = last;
+        if (last == 0) {
+          for (int j = n + 1 + lane; j < n_out; j += 32) s_list[beam][j] = 0;
+          break;
+        }
       }
     }
   }
   __syncthreads();
-  if (beam != 0) return;
-  const bool live = lane < beams && s_score[lane < beams ? lane : 0] > -INFINITY;
-  const double sc = live ? (double)s_score[lane] : 0.0;
-  const bool done = live && s_done[lane];
-  const double base = live && !done ? s_lse[lane] : 0.0;
-  int at = 0;
-  auto value = [&](unsigned &v) -> double {
-    if (!live) return -INFINITY;
-    if (done) {
-      v = (unsigned)eos;
-      return at == 0 ? sc : -INFINITY;
-    }
-    const unsigned long long k = at < n_out ? s_list[lane][at] : 0;
-    if (!k) return -INFINITY;
-    v = beam_key_index(k);
-    return ((double)beam_key_logit(k) - base) + sc;
-  };
-  unsigned v = 0;
-  double c = value(v);
-  for (int n = 0; n < n_out; ++n) {
-    // the lane with the largest c (the lowest lane of equal ones: beams are in
-    // lane order, so that is the lowest k V + v)
-    double m = c;
-    int who = lane;
+  unsigned rough = 0;  // beams whose log sum is the chunks' (warp 0)
+  for (bool first = true;; first = false) {
+    if (beam == 0) {
+      const bool live = lane < beams && s_score[lane < beams ? lane : 0] > -INFINITY;
+      const double sc = live ? (double)s_score[lane] : 0.0;
+      const bool done = live && s_done[lane];
+      const double base = live && !done ? s_lse[lane] : 0.0;
+      if (first) rough = __ballot_sync(0xffffffffu, live && !done);
+      int at = 0;
+      auto value = [&](unsigned &v) -> double {
+        if (!live) return -INFINITY;
+        if (done) {
+          v = (unsigned)eos;
+          return at == 0 ? sc : -INFINITY;
+        }
+        const unsigned long long k = at < n_out ? s_list[lane][at] : 0;
+        if (!k) return -INFINITY;
+        v = beam_key_index(k);
+        return ((double)beam_key_logit(k) - base) + sc;
+      };
+      unsigned v = 0;
+      double c = value(v), taken = 0.0;  // lane n: what slot n took, and whose
+      int from = -1;
+      for (int n = 0; n < n_out; ++n) {
+        // the lane with the largest c (the lowest lane of equal ones: beams are in
+        // lane order, so that is the lowest k V + v)
+        double m = c;
+        int who = lane;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const double mo = __shfl_xor_sync(0xffffffffu, m, o);
-      const int wo = __shfl_xor_sync(0xffffffffu, who, o);
-      if (mo > m || (mo == m && wo < who)) {
-        m = mo;
-        who = wo;
+        for (int o = 16; o >= 1; o >>= 1) {
+          const double mo = __shfl_xor_sync(0xffffffffu, m, o);
+          const int wo = __shfl_xor_sync(0xffffffffu, who, o);
+          if (mo > m || (mo == m && wo < who)) {
+            m = mo;
+            who = wo;
+          }
+        }
+        const long long o = (long long)blockIdx.x * n_out + n;
+        if (!(m > -INFINITY)) {
+          if (lane == 0) {
+            out_scores[o] = -INFINITY;
+            parent[o] = n % beams;
+            token[o] = -1;
+            if (out_finished) out_finished[o] = 0;
+          }
+        } else {
+          if (lane == n) {
+            taken = m;
+            from = who;
+          }
+          if (lane == who) {
+            out_scores[o] = fmaxf((float)c, -3.402823466e38f);
+            parent[o] = who;
+            token[o] = (int32_t)v;
+            if (out_finished) out_finished[o] = done || (int)v == eos;
+            ++at;
+            c = value(v);
+          }
+        }
+        __syncwarp();
       }
-    }
-    const long long o = (long long)blockIdx.x * n_out + n;
-    if (!(m > -INFINITY)) {
-      if (lane == 0) {
-        out_scores[o] = -INFINITY;
-        parent[o] = n % beams;
-        token[o] = -1;
-        if (out_finished) out_finished[o] = 0;
+      // the rough ones of beams a and b, worth ca >= cb, where the two lie too close
+      auto close = [&](int a, double ca, int b, double cb) {
+        const unsigned pair = rough & (1u << a | 1u << b);
+        return a != b && pair && ca - cb <= (pair & (pair - 1) ? 2.0 * tol : tol) ? pair : 0u;
+      };
+      unsigned redo = 0;
+      if (rough && beams > 1) {  // the same for the warp
+        const double before = __shfl_up_sync(0xffffffffu, taken, 1);
+        const int whose = __shfl_up_sync(0xffffffffu, from, 1);
+        const double least = __shfl_sync(0xffffffffu, taken, n_out - 1);
+        const int last = __shfl_sync(0xffffffffu, from, n_out - 1);
+        if (lane > 0 && from >= 0) redo = close(whose, before, from, taken);
+        if (last >= 0 && c > -INFINITY) redo |= close(last, least, lane, c);
+        redo = __reduce_or_sync(0xffffffffu, redo);
       }
-    } else if (lane == who) {
-      out_scores[o] = fmaxf((float)c, -3.402823466e38f);
-      parent[o] = who;
-      token[o] = (int32_t)v;
-      if (out_finished) out_finished[o] = done || (int)v == eos;
-      ++at;
-      c = value(v);
+      rough &= ~redo;
+      if (lane == 0) s_redo = redo;
     }
-    __syncwarp();
+    __syncthreads();
+    const unsigned redo = s_redo;
+    if (__builtin_expect(redo == 0, 1)) return;
+    for (unsigned r = redo; r; r &= r - 1) {
+      const int k = __ffs(r) - 1;
+      const double top = (double)s_top[k];
+      const double t =
+          beam_exact_sum(logits + ((long long)blockIdx.x * beams + k) * ld, V, top, s_part);
+      if (threadIdx.x == 0) s_lse[k] = top + log(t);
+    }
+    __syncthreads();
   }
 }
 

@@ -1,5 +1,5 @@
 """The token loop's operators at the borders of their definitions: exact ties of
-codes, the largest weights."""
+codes, the largest weights, candidates of different beams that lie close."""
 import math
 
 import pytest
@@ -110,3 +110,120 @@ def test_prepared_weights_of_the_largest_magnitudes(lib):
             with pytest.raises(lib.FmError) as e:
                 lib.sync_status()
             assert e.value.status == 5
+
+
+# ------------------------------------------------------------------ beam selection
+def check(lib, logits, scores, n_out, finished=None, eos=-1, exact=()):
+    B, k, V = logits.shape
+    out = torch.full((B, n_out), 77.0, device="cuda")
+    par, tok = (torch.full((B, n_out), 77, device="cuda", dtype=torch.int32) for _ in range(2))
+    fin = torch.full((B, n_out), 77, device="cuda", dtype=torch.uint8)
+    ws = torch.full((lib.beam_workspace_bytes(B, k, V, n_out),), 255, device="cuda", dtype=torch.uint8)
+    lib.beam_select(logits, scores, out, par, tok, ws, finished=finished, out_finished=fin, eos=eos)
+    lib.sync_status()
+    want = P.beam(logits.cpu(), scores.cpu(), None if finished is None else finished.cpu(), eos, n_out)
+    assert torch.equal(par.cpu().long(), want[1])
+    assert torch.equal(tok.cpu().long(), want[2])
+    assert torch.equal(fin.cpu(), want[3])
+    w, got = want[0], out.cpu().to(F64)
+    live = w > -torch.inf
+    assert torch.equal(got > -torch.inf, live)
+    # c is rounded once to fp32 after a log sum whose arguments are rounded three
+    # times in fp32 (2.25 * 2^-24 of ln V on average), whose exponentials are off
+    # by 2^-22, and of which 16 at a time are added in fp32 (15 * 2^-24)
+    tol = w.abs() * 2.0 ** -24 + (2.25 * math.log(V) + 20) * 2.0 ** -24
+    assert bool(((got - w).abs()[live] <= tol[live]).all())
+    return got, w
+
+
+def row(V, first, d, n):
+    """One logit of 0 at `first` and n of -d behind it, the rest masked."""
+    l = torch.full((V,), -math.inf)
+    l[first] = 0.0
+    l[first + 1:first + 1 + n] = -d
+    return l
+
+
+def lse(l):
+    return float(torch.logsumexp(l.to(F64), 0))
+
+
+def near_pair(V, d1, n1, d2, margin):
+    """Two rows and scores whose best candidates differ by `margin` (beam 1's is
+    worth more where it is positive)."""
+    a = row(V, 5, d1, n1)
+    b = row(V, 7, d2, round(n1 * math.exp(d2 - d1)))
+    return torch.stack([a, b]), torch.tensor([0.0, lse(b) - lse(a) + margin])
+
+
+PAIRS = [(9.5, 60000, 5.0), (5.0, 600, 9.5), (13.0, 99000, 10.25), (10.25, 6000, 13.0), (7.0, 90000, 2.75),
+         (11.5, 99000, 0.5)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n_out", [1, 2, 5])
+def test_select_between_close_beams(lib, n_out, dtype):
+    """Candidates of two beams that differ by less than fp32 tells apart are taken
+    in the order of their 64-bit values; alone and in a batch."""
+    V, cases = 100003, []
+    for d1, n1, d2 in PAIRS:
+        for m in (3e-8, 1e-7, 4e-7, 2e-6):
+            cases += [near_pair(V, d1, n1, d2, m), near_pair(V, d1, n1, d2, -m)]
+    logits = torch.stack([c[0] for c in cases]).to("cuda", dtype)
+    scores = torch.stack([c[1] for c in cases]).float().cuda()
+    check(lib, logits, scores, n_out)
+    for b in range(0, len(cases), 5):
+        check(lib, logits[b:b + 1].clone(), scores[b:b + 1].clone(), n_out)
+
+
+def test_select_among_many_close_beams(lib):
+    """Eight beams in a tangle, an ended beam among them, and one beam's second
+    candidate beside another's first."""
+    V, k, g = 30011, 8, torch.Generator().manual_seed(3)
+    logits, scores = torch.empty(4, k, V), torch.empty(4, k)
+    for b in range(4):
+        for j in range(k):
+            d = 2.0 + 9.0 * float(torch.rand((), generator=g))
+            l = row(V, 3 * j, d, min(20000, round(0.3 * math.exp(d))))
+            l[V - 1 - j] = -1e-7 * (j + 1)
+            logits[b, j] = l
+            scores[b, j] = lse(l) - 0.5 + 1e-6 * (float(torch.rand((), generator=g)) - 0.5)
+    scores[1:] += torch.tensor([0.0, -3.0, -40.0])[:, None]
+    fin = torch.zeros(4, k, dtype=torch.uint8)
+    fin[0, 2] = fin[2, 5] = 1
+    scores[0, 2], scores[2, 5] = -0.5, -3.5
+    for n_out in (1, 3, 8, 16):
+        check(lib, logits.cuda(), scores.cuda(), n_out, fin.cuda(), 11)
+        check(lib, logits[:1].cuda(), scores[:1].cuda(), n_out, fin[:1].cuda(), 11)
+
+
+@pytest.mark.parametrize("margin", [-1e-6, -2e-7, 2e-7, 1e-6])
+def test_select_with_an_ended_beam_between_two_close_ones(lib, margin):
+    """The one candidate taken, an ended beam's below it, and a third beam's that
+    only the 64-bit sums place."""
+    V = 100003
+    for d1, n1, d2 in PAIRS:
+        l, s = near_pair(V, d1, n1, d2, margin)
+        logits = torch.full((1, 3, V), -1.0)
+        logits[0, 0], logits[0, 2] = l[0], l[1]
+        first = -lse(l[0])
+        for below in (0.0, 1e-6, 2.7e-6, 4e-6):
+            scores = torch.tensor([[0.0, first - below, s[1]]])
+            fin = torch.tensor([[0, 1, 0]], dtype=torch.uint8)
+            for n_out in (1, 2, 3):
+                check(lib, logits.cuda(), scores.float().cuda(), n_out, fin.cuda(), 9)
+
+
+def test_select_between_close_beams_with_masks_and_odd_rows(lib):
+    """The same with NaN and infinite logits in the rows and rows of odd strides."""
+    V = 20011
+    wide = torch.full((2, 2, V + 5), 3.0)
+    scores = torch.zeros(2, 2)
+    for b, m in enumerate((1e-7, -1e-7)):
+        wide[b, :, :V], scores[b] = near_pair(V, 9.0, 15000, 4.5, m)
+    wide[:, :, 15:18] = math.nan
+    wide[:, 0, 18] = -math.inf
+    for b, m in enumerate((1e-7, -1e-7)):
+        l = torch.nan_to_num(wide[b, :, :V].to(F64), nan=-math.inf, neginf=-math.inf)
+        scores[b, 1] = scores[b, 0] + lse(l[1]) - lse(l[0]) + m
+    check(lib, wide.cuda()[:, :, :V], scores.cuda(), 4)
