@@ -683,7 +683,7 @@ fm_status fm_embed_rows(const int32_t *ids, int64_t M, const void *table, fm_dty
  * n_out = beams.  beams and n_out in [1, 32]; n_out = beams = 1 is greedy
  * decoding; beams = 1 with n_out > 1 opens a search.
  * ws: device workspace of fm_beam_workspace_bytes(B, beams, V, n_out) bytes
- * (0 for invalid sizes), written before it is read; calls that may overlap on
+ * (0 for invalid sizes; enough for every smaller B, beams, V and n_out too), written before it is read; calls that may overlap on
  * the GPU (other streams, other captured graphs) need one each.  The logits of
  * a beam that is finished or dead are not read. */
 size_t fm_beam_workspace_bytes(int B, int beams, int64_t V, int n_out);

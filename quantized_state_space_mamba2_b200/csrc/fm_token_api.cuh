@@ -178,26 +178,32 @@ extern "C" fm_status fm_fp8_gemm(const void *A, const float *s_a, int64_t M, con
 
 // ------------------------------------------------------------------ beam selection
 // Logits per thread of a chunk: 16, or 8 for the latency of selections that
-// would give an SM (of 148) less than two chunks of 16.
-static int beam_elems(int64_t rows, int64_t V) {
-  return rows * ((V + kBeamThreads * 16 - 1) / (kBeamThreads * 16)) >= 296 ? 16 : 8;
+// would give an SM less than two chunks of 16.
+static int64_t beam_chunks_of(int elems, int64_t V) {
+  return (V + kBeamThreads * elems - 1) / (kBeamThreads * elems);
 }
-static int64_t beam_chunks(int64_t rows, int64_t V) {
-  const int64_t n = kBeamThreads * beam_elems(rows, V);
-  return (V + n - 1) / n;
+static int beam_elems(int64_t rows, int64_t V) {
+  return rows * beam_chunks_of(16, V) >= 2 * sm_count() ? 16 : 8;
+}
+// The most chunks that a selection of up to `rows` rows and V logits has: more rows
+// can have fewer of them, where they change from 8 to 16 logits per thread.  With 8
+// there are at most twice as many as there would be of 16, which is less than 2
+// per SM.
+static int64_t beam_most_chunks(int64_t rows, int64_t V) {
+  return std::max(rows * beam_chunks_of(16, V),
+                  std::min<int64_t>(rows * beam_chunks_of(8, V), 2 * (2 * sm_count() - 1)));
 }
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 static bool beam_sizes_ok(int B, int beams, int64_t V, int n_out) {
   return B >= 0 && beams >= 1 && beams <= kBeamMax && n_out >= 1 && n_out <= kBeamMax && V >= 1 &&
          V <= 0x7FFFFFFF && (int64_t)B * beams <= 0x7FFFFFFF &&
-         (int64_t)B * beams * beam_chunks((int64_t)B * beams, V) <= 0x7FFFFFFF;
+         beam_most_chunks((int64_t)B * beams, V) <= 0x7FFFFFFF;
 }
 
 extern "C" size_t fm_beam_workspace_bytes(int B, int beams, int64_t V, int n_out) {
   if (!beam_sizes_ok(B, beams, V, n_out)) return 0;
-  const int64_t rows = (int64_t)B * beams;
-  const size_t chunks = (size_t)rows * beam_chunks(rows, V);
+  const size_t chunks = (size_t)beam_most_chunks((int64_t)B * beams, V);
   return round256(chunks * n_out * 8) + round256(chunks * 8) + round256(chunks * 4);
 }
 
@@ -231,7 +237,7 @@ extern "C" fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t l
     return fail(FM_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", __func__, need);
   NEED(ws);
   const int64_t rows = (int64_t)B * beams;
-  const int S = (int)beam_chunks(rows, V), E = beam_elems(rows, V);
+  const int E = beam_elems(rows, V), S = (int)beam_chunks_of(E, V);
   const size_t chunks = (size_t)rows * S;
   unsigned long long *keys = (unsigned long long *)ws;
   double *sums = (double *)((char *)ws + round256(chunks * n_out * 8));

@@ -113,12 +113,13 @@ def test_prepared_weights_of_the_largest_magnitudes(lib):
 
 
 # ------------------------------------------------------------------ beam selection
-def check(lib, logits, scores, n_out, finished=None, eos=-1, exact=()):
+def check(lib, logits, scores, n_out, finished=None, eos=-1, ws=None):
     B, k, V = logits.shape
     out = torch.full((B, n_out), 77.0, device="cuda")
     par, tok = (torch.full((B, n_out), 77, device="cuda", dtype=torch.int32) for _ in range(2))
     fin = torch.full((B, n_out), 77, device="cuda", dtype=torch.uint8)
-    ws = torch.full((lib.beam_workspace_bytes(B, k, V, n_out),), 255, device="cuda", dtype=torch.uint8)
+    if ws is None:
+        ws = torch.full((lib.beam_workspace_bytes(B, k, V, n_out),), 255, device="cuda", dtype=torch.uint8)
     lib.beam_select(logits, scores, out, par, tok, ws, finished=finished, out_finished=fin, eos=eos)
     lib.sync_status()
     want = P.beam(logits.cpu(), scores.cpu(), None if finished is None else finished.cpu(), eos, n_out)
@@ -227,3 +228,15 @@ def test_select_between_close_beams_with_masks_and_odd_rows(lib):
         l = torch.nan_to_num(wide[b, :, :V].to(F64), nan=-math.inf, neginf=-math.inf)
         scores[b, 1] = scores[b, 0] + lse(l[1]) - lse(l[0]) + m
     check(lib, wide.cuda()[:, :, :V], scores.cuda(), 4)
+
+
+def test_select_with_one_workspace_for_a_shrinking_batch(lib):
+    """A workspace sized for the largest batch serves every smaller one."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    V, n = 50000, 8
+    ws = torch.empty(lib.beam_workspace_bytes(13, 2, V, n), device="cuda", dtype=torch.uint8)
+    assert lib.beam_workspace_bytes(1, 1, 1, 1) > 0
+    logits = torch.randn(13, 2, V, device="cuda", generator=g)
+    scores = -torch.rand(13, 2, device="cuda", generator=g)
+    for B in (13, 12, 11, 10, 4, 1):
+        check(lib, logits[:B], scores[:B], n, ws=ws)

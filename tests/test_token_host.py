@@ -299,3 +299,20 @@ def test_a_layer_on_a_side_stream_owns_its_buffers(monkeypatch):
         call()
         assert made and set(made) == {"side"} and ran and set(ran) == {"side"}
         assert now[0] is None
+
+
+def test_beam_workspace_covers_smaller_selections(so):
+    """A workspace sized for a selection serves every one of fewer sequences, beams,
+    tokens or slots."""
+    size = so.fm_beam_workspace_bytes
+    for V in (1, 2048, 2049, 4096, 4097, 8193, 32001, 50000, 100003, 1 << 20, (1 << 31) - 1):
+        for n in (1, 4, 8, 32):
+            rows = [size(B, 1, V, n) for B in range(0, 320)]
+            assert rows == sorted(rows), (V, n)
+            for B in (1, 5, 12, 40):
+                beams = [size(B, k, V, n) for k in range(1, 33)]
+                assert beams == sorted(beams), (B, V, n)
+            assert [size(7, 3, V, m) for m in range(1, 33)] == sorted(size(7, 3, V, m) for m in range(1, 33))
+    for rows in (1, 3, 12, 40, 150, 300):
+        by_v = [size(rows, 2, V, 4) for V in range(1, 200001, 511)]
+        assert by_v == sorted(by_v), rows
