@@ -621,8 +621,8 @@ typedef enum fm_dtype { FM_F32 = 0, FM_BF16 = 1, FM_E4M3 = 2, FM_I8 = 3 } fm_dty
  * bits).  A block or row whose max|y| is below 2^-100 has s = 0 and codes 0.
  *   x        [M, K] FM_F32 or FM_BF16, rows ldx elements apart
  *   residual [M, K] fp32, rows ldr apart, or NULL
- *   sum_out  [M, K] fp32, rows lds apart, or NULL: receives r; may be x or
- *            residual itself (same address and row stride)
+ *   sum_out  [M, K] fp32, rows lds apart, or NULL: receives r; may be x (where
+ *            that is FM_F32) or residual itself (same address and row stride)
  *   q        [M, K] dense
  * K % 16 == 0, K <= 16384; row strides are multiples of 4 elements; eps in
  * [1e-30, 1e30]. */

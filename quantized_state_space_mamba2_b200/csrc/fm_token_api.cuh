@@ -41,6 +41,11 @@ extern "C" fm_status fm_add_norm_quant(const void *x, fm_dtype x_type, int64_t l
   if (ldx < K || ldx % 4 || (residual && (ldr < K || ldr % 4)) || (sum_out && (lds < K || lds % 4)))
     return fail(FM_ERR_SHAPE, "%s: row strides must be multiples of 4, at least K", __func__);
   if (M == 0) return FM_OK;
+  // a sum written over an input must fall on the element that it is the sum of
+  if (sum_out && ((sum_out == x && (x_type != FM_F32 || (M > 1 && lds != ldx))) ||
+                  (sum_out == residual && M > 1 && lds != ldr)))
+    return fail(FM_ERR_INVALID_ARG, "%s: sum_out replaces an input of another type or row stride",
+                __func__);
   NEED(x);
   OPT(residual);
   NEED(norm_w);

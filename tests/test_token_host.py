@@ -316,3 +316,12 @@ def test_beam_workspace_covers_smaller_selections(so):
     for rows in (1, 3, 12, 40, 150, 300):
         by_v = [size(rows, 2, V, 4) for V in range(1, 200001, 511)]
         assert by_v == sorted(by_v), rows
+
+
+def test_norm_refuses_sums_over_inputs_of_another_layout(so):
+    """sum_out may be x or the residual only where each element lands on itself."""
+    assert norm(so, xt=1, out=p[0]) == ARG                # bf16 x: the sums are twice as wide
+    assert norm(so, ldx=264, out=p[0]) == ARG             # other row strides
+    assert norm(so, out=p[0], lds=264) == ARG
+    assert norm(so, ldr=260, out=p[1]) == ARG
+    assert norm(so, M=0, xt=1, out=p[0]) == OK
