@@ -701,7 +701,7 @@ fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t ld, int B, i
  * [0, src_beams) leaves its row as it was and raises FM_ERR_INDEX at the next
  * fm_sync_status.  src, dst and row_bytes are host arrays, read before the
  * call returns; parent [B, dst_beams] is on the device.  Buffers of one call
- * may not overlap each other.  Beams in [1, 32], B <= 65535. */
+ * may overlap neither each other nor parent.  Beams in [1, 32], B <= 65535. */
 fm_status fm_reorder_rows(const void *const *src, void *const *dst, const int64_t *row_bytes,
                           int n_bufs, int B, int src_beams, int dst_beams, const int32_t *parent,
                           fm_stream stream);

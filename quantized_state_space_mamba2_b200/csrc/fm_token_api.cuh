@@ -315,6 +315,11 @@ extern "C" fm_status fm_reorder_rows(const void *const *src, void *const *dst,
                d0 < s0 + (uintptr_t)(row_bytes[i] * B * src_beams)) {
       return fail(FM_ERR_INVALID_ARG, "%s: src and dst of buffer %d overlap", __func__, i);
     }
+    // the parents are read by every block, before and after others have written
+    const uintptr_t p0 = (uintptr_t)parent;
+    if (row_bytes[i] && d0 < p0 + (uintptr_t)B * dst_beams * 4 &&
+        p0 < d0 + (uintptr_t)(row_bytes[i] * B * dst_beams))
+      return fail(FM_ERR_INVALID_ARG, "%s: buffer %d overlaps the parents", __func__, i);
   }
   // one launch per 128 buffers of the same unit: 16 bytes where the rows are
   // multiples of 16 (every state of the library), else 4 or 1

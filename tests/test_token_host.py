@@ -325,3 +325,17 @@ def test_norm_refuses_sums_over_inputs_of_another_layout(so):
     assert norm(so, out=p[0], lds=264) == ARG
     assert norm(so, ldr=260, out=p[1]) == ARG
     assert norm(so, M=0, xt=1, out=p[0]) == OK
+
+
+def test_reorder_refuses_to_write_the_parents(so):
+    def arr(*v):
+        return (C.c_void_p * len(v))(*v)
+
+    def ro(src, dst, nbytes, B=2, sb=4, db=4, par=0x900000):
+        n = len(nbytes)
+        return so.fm_reorder_rows(arr(*src), arr(*dst), (C.c_int64 * n)(*nbytes), n, B, sb, db, par, None)
+
+    # the parents are read while the buffers are written: 2 x 4 of 4 bytes at 0x900000
+    for at, rb in ((0x900000, 4), (0x900010, 4), (0x8FFFF0, 64), (0x8FF000, 0x300)):
+        assert ro([at], [at], [rb]) == ARG, (at, rb)
+        assert ro([0x100000, 0x200000], [0x100000, at], [64, rb]) == ARG, (at, rb)
