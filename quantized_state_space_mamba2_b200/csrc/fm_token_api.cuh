@@ -289,6 +289,12 @@ static fm_status launch_reorder(const ReorderArgs &a, unsigned blocks, int B, cu
   return launched("k_reorder_rows");
 }
 
+// Bytes that a thread moves of a row at once: 16 where the rows are multiples of
+// 16 (every state of the library), else 4 or 1.
+static int reorder_unit(int64_t row_bytes) {
+  return row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : 1;
+}
+
 extern "C" fm_status fm_reorder_rows(const void *const *src, void *const *dst,
                                      const int64_t *row_bytes, int n_bufs, int B, int src_beams,
                                      int dst_beams, const int32_t *parent, fm_stream stream) {
@@ -300,8 +306,9 @@ extern "C" fm_status fm_reorder_rows(const void *const *src, void *const *dst,
   if (B == 0 || n_bufs == 0) return FM_OK;
   NEED(parent);
   for (int i = 0; i < n_bufs; ++i) {
-    if (row_bytes[i] < 0 || row_bytes[i] > (int64_t)1 << 36)
-      return fail(FM_ERR_SHAPE, "%s: row_bytes[%d] is negative or above 2^36", __func__, i);
+    // a launch counts a row's units in 32 bits
+    if (row_bytes[i] < 0 || row_bytes[i] / reorder_unit(row_bytes[i]) > 0xFFFFFFFFll)
+      return fail(FM_ERR_SHAPE, "%s: row_bytes[%d] is negative or too long", __func__, i);
     if (row_bytes[i] && (!src[i] || !dst[i]))
       return fail(FM_ERR_INVALID_ARG, "%s: buffer %d is null", __func__, i);
     if (!aligned16(src[i]) || !aligned16(dst[i]))
@@ -321,8 +328,7 @@ extern "C" fm_status fm_reorder_rows(const void *const *src, void *const *dst,
         p0 < d0 + (uintptr_t)(row_bytes[i] * B * dst_beams))
       return fail(FM_ERR_INVALID_ARG, "%s: buffer %d overlaps the parents", __func__, i);
   }
-  // one launch per 128 buffers of the same unit: 16 bytes where the rows are
-  // multiples of 16 (every state of the library), else 4 or 1
+  // one launch per 128 buffers of the same unit
   for (int unit : {16, 4, 1}) {
     ReorderArgs a = {};
     a.src_beams = src_beams;
@@ -341,10 +347,8 @@ extern "C" fm_status fm_reorder_rows(const void *const *src, void *const *dst,
     };
     for (int i = 0; i < n_bufs; ++i) {
       const int64_t rb = row_bytes[i];
-      if (rb == 0 || unit != (rb % 16 == 0 ? 16 : rb % 4 == 0 ? 4 : 1)) continue;
+      if (rb == 0 || unit != reorder_unit(rb)) continue;
       const int64_t units = rb / unit, nb = (units + kReorderThreads - 1) / kReorderThreads;
-      if (units > 0xFFFFFFFFll || nb > 0x7FFFFFFFll)
-        return fail(FM_ERR_SHAPE, "%s: rows of buffer %d are too long", __func__, i);
       if (a.n == kReorderBufs || blocks + nb > 0x7FFFFFFFll) FM_TRY(flush());
       a.src[a.n] = src[i];
       a.dst[a.n] = dst[i];

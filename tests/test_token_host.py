@@ -339,3 +339,18 @@ def test_reorder_refuses_to_write_the_parents(so):
     for at, rb in ((0x900000, 4), (0x900010, 4), (0x8FFFF0, 64), (0x8FF000, 0x300)):
         assert ro([at], [at], [rb]) == ARG, (at, rb)
         assert ro([0x100000, 0x200000], [0x100000, at], [64, rb]) == ARG, (at, rb)
+
+
+def test_reorder_refuses_before_any_row_moves(so):
+    """Rows too long for a launch are refused before another buffer's are moved."""
+    def arr(*v):
+        return (C.c_void_p * len(v))(*v)
+
+    def ro(src, nbytes):
+        n = len(nbytes)
+        return so.fm_reorder_rows(arr(*src), arr(*src), (C.c_int64 * n)(*nbytes), n, 2, 4, 4, 1 << 50, None)
+
+    long = (1 << 32) + 1  # bytes: no multiple of 4, moved one by one
+    assert ro([0x100000], [long]) == SHAPE
+    assert ro([1 << 44, 0x100000], [64, long]) == SHAPE
+    assert ro([1 << 44, 0x100000], [64, 1 << 36]) == SHAPE
