@@ -111,10 +111,13 @@ static fm_status launch_fp8_large(const void *A, const void *W, long long K, Fp8
   auto kern = k_fp8_gemm_tc<BN, STAGES, TY>;
   // the warpgroups' register shares must fit what the block is launched with
   // (a share that does not would wait for ever)
-  static const int regs = [] {
+  static std::atomic<int> known{0};  // of this variant; a query that failed is made again
+  int regs = known.load(std::memory_order_relaxed);
+  if (!regs) {
     cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, k_fp8_gemm_tc<BN, STAGES, TY>) == cudaSuccess ? fa.numRegs : 0;
-  }();
+    FM_CHECK_CUDA(cudaFuncGetAttributes(&fa, kern));
+    known.store(regs = fa.numRegs, std::memory_order_relaxed);
+  }
   if (regs * kFp8Threads < 128 * kFp8RegsLoad + (kFp8Threads - 128) * kFp8RegsAcc)
     return fail(FM_ERR_UNSUPPORTED, "k_fp8_gemm_tc: built with %d registers per thread", regs);
   FM_CHECK_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kBytes));
