@@ -650,7 +650,8 @@ class RowSet:
     reordered in place.  Holds the tensors and the pointer arrays of the call."""
 
     def __init__(self, dst, src=None):
-        self.dst, self.src = list(dst), list(dst if src is None else src)
+        self.dst = list(dst)
+        self.src = list(self.dst if src is None else src)
         if len(self.dst) != len(self.src):
             raise ValueError("RowSet: as many src as dst tensors are required")
         n = len(self.dst)

@@ -354,3 +354,14 @@ def test_reorder_refuses_before_any_row_moves(so):
     assert ro([0x100000], [long]) == SHAPE
     assert ro([1 << 44, 0x100000], [64, long]) == SHAPE
     assert ro([1 << 44, 0x100000], [64, 1 << 36]) == SHAPE
+
+
+def test_row_set_of_any_iterable(monkeypatch):
+    """A RowSet keeps the tensors of a generator for both sides."""
+    from quantized_state_space_mamba2_b200 import lib
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # host tensors stand for the device's
+    buffers = [torch.zeros(8, 4), torch.zeros(8, 3)]
+    rows = lib.RowSet(t for t in buffers)
+    assert all(a is b for side in (rows.dst, rows.src) for a, b in zip(side, buffers))
+    assert len(rows.dst) == len(rows.src) == 2
+    assert list(rows._dst) == list(rows._src) == [t.data_ptr() for t in buffers]
