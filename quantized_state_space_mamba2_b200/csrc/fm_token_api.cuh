@@ -268,8 +268,8 @@ extern "C" fm_status fm_beam_select(const void *logits, fm_dtype type, int64_t l
   const double tol = (2.25 * std::log((double)V) + 20.0) * 0x1p-24;
   // an SM holds 32 warps of the merge: as many each as lets its entries run side by
   // side (one beam has no other to be close to)
-  const int per_sm = (B + sm_count() - 1) / sm_count();
-  const int warps = beams == 1 ? 1 : std::max(beams, 32 / per_sm);
+  const int64_t per_sm = ((int64_t)B + sm_count() - 1) / sm_count();
+  const int warps = beams == 1 ? 1 : std::max(beams, (int)(32 / per_sm));
   auto merge = [&](auto t) -> fm_status {
     using T = decltype(t);
     return launch_ex("k_beam_merge", k_beam_merge<T>, (unsigned)B, 32 * warps, 0, st, (const unsigned long long *)keys,
