@@ -639,8 +639,9 @@ fm_status fm_prepare_linear_fp8(const float *W, int64_t N, int64_t K, void *Wq, 
 
 /* Matrix product in 8-bit floating point with a scale for each block of 128:
  *   Y[m,n] = sum_b s_a[m,b] s_w[n/128,b] sum_{k in block b} A[m,k] W[n,k]
- * with fp32 sums, each block's sum scaled in fp32 and the total rounded once
- * to Y's type (FM_F32 or FM_BF16).
+ * with fp32 sums, each block's sum scaled in fp32 by fl(s_a s_w) and the total
+ * rounded once to Y's type (FM_F32 or FM_BF16).  s_a s_w has to be an fp32 number:
+ * above its range a block gives infinities and NaN, below it loses bits.
  *   A [M, K] e4m3, s_a [M, ceil(K/128)]; W [N, K] e4m3, s_w [ceil(N/128),
  *   ceil(K/128)]; Y rows ldy elements apart (any ldy >= N; other columns are
  *   left as they were).  K % 16 == 0; M, N any (0: nothing is done). */

@@ -7,14 +7,17 @@
 // are enough.  k_beam_chunks reads the logits once: a CTA holds a chunk of one
 // beam's row in registers and leaves its maximum, its sum of exponentials and
 // its n largest logits; k_beam_merge joins the chunks' sums and lists and takes
-// the n best of the beams' lists, by c in 64 bits.
+// the n best of the beams' lists by c, whose log sums it forms again in 64 bits
+// where the fp32 exponentials do not tell which candidate is worth more.
 //
 // What bounds it is the chain of each chunk (its loads, the maxima, the sum, the
 // few candidates), so an SM holds as many chunks as its 64 warps allow: 16
-// logits per thread, 8 CTAs.  64 x 8 x 100003 bf16, a fifth of the beams
-// finished: 53.6 us, 1.9 TB/s of logits (32 per thread, 4 CTAs: 61.7; 8 per
-// thread: 88; a warp by itself over a span of the row, without barriers: 73, its
-// code and registers too large).  The n largest of a chunk are found without
+// logits per thread, 8 CTAs (32 registers per thread; 56 bytes of a bf16 thread's
+// and 88 of an fp32 one's do not fit and are spilled).  64 x 8 x 100003 bf16, a
+// fifth of the beams finished and so not read: 53.6 us for the 80 MB of the others,
+// 1.5 TB/s (32 per thread, 4 CTAs: 61.7; 8 per thread: 88; a warp by itself over a
+// span of the row, without barriers: 73, its code and registers too large).
+// The n largest of a chunk are found without
 // sorting it: the n-th largest of 32 group maxima (groups of 8 threads) is not
 // above the chunk's n-th largest value, so few values reach it; they are
 // collected and ranked against each other.  Where ties or masks let more than
@@ -289,8 +292,9 @@ __device__ __forceinline__ double beam_exact_sum(const T *__restrict__ row, unsi
 // Compared are neighbours in the merged order of different beams (gaps that each
 // exceed both beams' errors add up to more than those of the two ends), and the
 // last one taken with the head of each list.  Random logits call for it in some
-// 10^-4 of the entries; rows that are equal, with equal scores, always (64 x 8 x
-// 100003 bf16: 509 us then, 53.8 us on random logits; 1760 us with 8 warps per
+// 10^-4 of the entries, for which they pay the comparison (1 x 4 x 32001 7.3 us in a
+// graph, 6.8 without); equal rows with equal scores call for it always (64 x 8 x
+// 100003 bf16: 509 us then, 53.6 us on random logits; 1760 us with 8 warps per
 // CTA).  More warps than beams are there for that work alone.
 
 template <typename T>

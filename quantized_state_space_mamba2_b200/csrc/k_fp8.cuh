@@ -9,16 +9,20 @@
 // TMEM accumulators form a ring, so the read-back of block b overlaps the
 // MMAs of the blocks after it.
 //
-// Large M (8192 x 10576 x 2560, bf16 out): 254 us, 1.75 PFLOP/s.  By cycles
+// Large M (8192 x 10576 x 2560, bf16 out): 258 us, 1.72 PFLOP/s.  By cycles
 // (4096 rows, one clock): the MMAs alone 109 k, with their loads 128 k, with the
-// hand-over of the two TMEM buffers 150 k, with the read-back and the scaling
+// hand-over of the two TMEM buffers 149 k, with the read-back and the scaling
 // 173 k: the hand-over and the read-back, a chain per block, bound it, and in a
-// loop the 1 kW power cap (1.5-1.8 GHz).  Pairs of CTAs (cta_group::2, 256 x 256
-// tiles, half the bytes per MMA) measured 196 k: the hand-over across CTAs is
-// longer than what the loads save.
-// Small M (64 x 50000 x 2560, fp32 out): 30.6 us, 4.6 TB/s; 16 rows 26.2 us, 5.0
-// TB/s.  The weight stream bounds it from below; the rest is the per-block chain
-// of the read-back where many rows wait for it.
+// loop the 1 kW power cap (1.5-1.8 GHz; codes and positive scales drawn evenly take
+// less power: 216 us).  Pairs of CTAs (cta_group::2, 256 x 256 tiles, half the bytes
+// per MMA) measured 196 k, in a version whose second CTA passed its loads on to the
+// leader through a warp of its own.  Output rows that are no multiple of 16 bytes are
+// stored element by element by the accumulator warps: N = 10575 302 us where N =
+// 10576 takes 216, at K = 256 151 and 48.
+// Small M (64 x 50000 x 2560, fp32 out): 31.4 us, 4.5 TB/s; 16 rows 26.0 us, 5.0
+// TB/s.  The weight stream bounds it from below; above that are the last wave (391
+// weight tiles on 148 SMs run as 3 waves, 12 % of the machine idle) and, where many
+// rows wait for it, the per-block chain of the read-back.
 #pragma once
 #include <cuda_bf16.h>
 #include "k_gemm.cuh"

@@ -50,10 +50,17 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
 // lane l of them the four groups of 4 columns at 4 l + 32 j, so every load of
 // the 8 lanes is one run of 128 bytes (fp32) and a block's maximum takes three
 // shuffles.  A row stays in registers: one read of x and residual, one write of
-// the sum, the codes and the scales; the weights are read once per CTA.  Up to
-// kNormAheadK columns the next row is on its way while this one is computed
-// (8192 x 2560 fp32 with residual: 51 us, 5.3 TB/s, bound by instruction issue;
-// 63.5 us with each row's loads waited for by themselves).
+// the sum, the codes and the scales; the weights are read once per CTA.
+//
+// Up to kNormAheadK columns the next row is on its way while this one is computed:
+// 8192 x 2560 fp32 with residual 51 us, 5.3 TB/s, bound by instruction issue.  Wider
+// rows, whose 11 to 32 warps leave no registers for a second row, take the variant
+// with one CTA per row, which waits for its loads (2048 x 8192: 49 us, 4.4 TB/s;
+// 1024 x 16384: 60 us, 3.7 TB/s; 64 registers, 40 bytes of them spilled).  At
+// widths that both can run (fp32 with residual to e4m3): 4096 x 5120 47.5 us ahead,
+// 57.2 one per row; 4096 x 2560 25.9 and 28.2; 64 x 2560 3.2 and 3.4.  Rows of one
+// or two warps, a row or two per CTA, are bound by the chain of a row (loads,
+// barriers) either way: 2049 x 768 bf16 to int8 6.7 and 6.5 us.
 constexpr int kNormCols = 512;   // columns per warp
 constexpr int kNormMaxK = 32 * kNormCols;
 constexpr int kNormAheadWarps = 10, kNormAheadK = kNormAheadWarps * kNormCols;
@@ -261,7 +268,8 @@ __global__ void __launch_bounds__(kAhead ? 32 * kNormAheadWarps : 1024, kAhead ?
 }
 
 // Offline: W [N, K] fp32 -> e4m3 codes and one scale per 128 x 128 block,
-// s = fl(max|W| / 448), code = nearest(W / s).  One CTA of 256 threads per block.
+// s = fl(max|W| / 448), code = nearest(W / s).  One CTA of 256 threads per block,
+// which reads it twice (50000 x 2560: 211 us, 3.0 TB/s of weights and codes).
 __global__ void __launch_bounds__(256) k_prepare_linear_fp8(const float *__restrict__ W, long long N,
                                                             int K, uint8_t *__restrict__ Wq,
                                                             float *__restrict__ s_w) {
@@ -357,8 +365,8 @@ __global__ void __launch_bounds__(128) k_embed_rows(const int32_t *__restrict__ 
 // parent outside the source's beams leaves the row as it was and sets the
 // device error word.  Like every kernel that writes a carried state it issues no
 // early trigger: k_scan_step loads its state before its dependency wait.
-// Bound by memory: 64 layers of 4 x 8 beams, 5.4 GB of int32 states, 1.2 ms, 6.6
-// TB/s of what has to move.
+// Bound by memory: 64 layers of 4 x 8 beams, 5.4 GB of int32 states, 1.15 ms, 7.0
+// TB/s of what has to move (source rows that several beams take come from L2).
 constexpr int kReorderBufs = 128;  // buffers per launch
 constexpr int kReorderBeams = 32;
 constexpr int kReorderThreads = 256;
