@@ -291,11 +291,11 @@ __device__ __forceinline__ double beam_exact_sum(const T *__restrict__ row, unsi
 // then formed again, in 64 bits from the logits, and the lists merged once more.
 // Compared are neighbours in the merged order of different beams (gaps that each
 // exceed both beams' errors add up to more than those of the two ends), and the
-// last one taken with the head of each list.  Random logits call for it in some
-// 10^-4 of the entries, for which they pay the comparison (1 x 4 x 32001 7.3 us in a
-// graph, 6.8 without); equal rows with equal scores call for it always (64 x 8 x
-// 100003 bf16: 509 us then, 53.6 us on random logits; 1760 us with 8 warps per
-// CTA).  More warps than beams are there for that work alone.
+// last one taken with the head of each list: 0.5 us (1 x 4 x 32001 in a graph 7.3
+// us, 6.8 without).  Random logits call for new sums in some 10^-4 of the entries,
+// equal rows with equal scores always (64 x 8 x 100003 bf16: 509 us then, 53.6 us
+// on random logits; 1760 us with 8 warps per CTA).  More warps than beams are there
+// for that work alone.
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kBeamMax)
